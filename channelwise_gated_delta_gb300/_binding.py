@@ -39,7 +39,8 @@ STATUS_NAMES = {0: "GDR_OK", 1: "GDR_ERR_NULL", 2: "GDR_ERR_SHAPE", 3: "GDR_ERR_
 EXPORTED = ("gdr_workspace_bytes", "gdr_set_workspace", "gdr_forward_ex", "gdr_forward",
             "gdr_forward_chunked_noalloc",
             "gdr_varlen_workspace_bytes", "gdr_forward_varlen", "gdr_tree_workspace_bytes",
-            "gdr_forward_tree", "gdr_host_staging_bytes", "gdr_forward_host", "gdr_device_check",
+            "gdr_forward_tree", "gdr_verify_drafts", "gdr_commit_path", "gdr_state_store",
+            "gdr_state_load", "gdr_host_staging_bytes", "gdr_forward_host", "gdr_device_check",
             "gdr_trace_enable", "gdr_trace_read", "gdr_status_string",
             "gdr_last_cuda_error", "gdr_version")
 
@@ -83,6 +84,15 @@ def load_library(path=LIB_PATH):
     lib.gdr_tree_workspace_bytes.restype = sz
     lib.gdr_forward_tree.argtypes = [vp] * 7 + [ip] + [i] * 6 + [vp, i, vp, sz, u]
     lib.gdr_forward_tree.restype = i
+    ll = ctypes.c_longlong
+    lib.gdr_verify_drafts.argtypes = [vp] * 9 + [i] * 3 + [ll] * 4 + [i, vp, i]
+    lib.gdr_verify_drafts.restype = i
+    lib.gdr_commit_path.argtypes = [vp] * 8 + [i] * 7 + [vp, i, u]
+    lib.gdr_commit_path.restype = i
+    lib.gdr_state_store.argtypes = [vp] * 4 + [i] * 5 + [vp]
+    lib.gdr_state_store.restype = i
+    lib.gdr_state_load.argtypes = [vp] * 4 + [i] * 5 + [vp]
+    lib.gdr_state_load.restype = i
     lib.gdr_host_staging_bytes.argtypes = [i] * 8
     lib.gdr_host_staging_bytes.restype = sz
     lib.gdr_forward_host.argtypes = fwd + [vp, sz]
@@ -117,12 +127,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _dtype_code(dt):
+def _dtype_code(dt, what="q/k/v"):
     if dt == torch.bfloat16:
         return GDR_BF16
     if dt == torch.float32:
         return GDR_F32
-    raise TypeError("q/k/v must be bfloat16 or float32, got %s" % dt)
+    raise TypeError("%s must be bfloat16 or float32, got %s" % (what, dt))
 
 
 def gdr_workspace_bytes(B, T, HK, HV, dk, dv, chunk=64, dtype=torch.bfloat16, flags=0):
@@ -339,6 +349,179 @@ def gdr_forward_tree(q, k, v, g, beta, parent, h0=None, out=None, stream=None, w
                               par_c, B, T, HK, HV, dk, dv, ctypes.c_void_p(stream.cuda_stream), code,
                               ws_ptr, ws_bytes, flags)
     _check(lib, st)
+    return out
+
+
+def _on_device(dev, *named):
+    """Every named tensor that is given is on the CUDA device ``dev`` and contiguous."""
+    if dev.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor" % named[0][0])
+    for name, t in named:
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError("%s must be a CUDA tensor on %s" % (name, dev))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _is(name, t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s %s, got %s %s"
+                         % (name, dtype, list(shape), t.dtype, list(t.shape)))
+
+
+def _prob_rows(name, t):
+    """The distance of the rows of [B, T, V] probabilities, whose rows may be apart."""
+    B, T, V = t.shape
+    ld = t.stride(1) if T > 1 else t.stride(0) if B > 1 else V
+    if (V > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != T * ld) or ld < V:
+        raise ValueError("%s must have rows of adjacent elements at one distance" % name)
+    return ld
+
+
+def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=None, n_path=None,
+                      next_token=None, stream=None):
+    """Verification of draft trees against the target's probabilities (include/gdr.h has the rule).
+
+    p [B, T, V] (f32 or bf16): the target's distribution after each node; q the same shape and
+    dtype: what the node's children were drawn from, or None where they were proposed.  Their
+    rows may be further apart than V (a slice of a padded tensor).  tokens, parent [B, T] int32,
+    node 0 the root; parent may have any strides (one tree for the batch: tree.expand(B, T)).
+    coins [B, T] and u [B] f32 random numbers in [0, 1).  All on the GPU.
+    Returns (path [B, max_path], n_path [B], next_token [B]), int32: the accepted nodes, -1
+    behind them, how many, and the next token; allocated when not given.  max_path defaults to T.
+    """
+    lib = load_library()
+    if p.dim() != 3:
+        raise ValueError("p must be [B, T, V]")
+    B, T, V = p.shape
+    dev = p.device
+    code = _dtype_code(p.dtype, "p and q")
+    if max_path is None:
+        max_path = T if path is None else path.shape[-1]
+    _on_device(dev, ("tokens", tokens), ("coins", coins), ("u", u), ("path", path),
+               ("n_path", n_path), ("next_token", next_token))
+    for name, t in (("parent", parent), ("q", q)):  # of any strides: checked below
+        if t is not None and t.device != dev:
+            raise ValueError("%s must be a CUDA tensor on %s" % (name, dev))
+    if q is not None:
+        _is("q", q, p.shape, p.dtype)
+    _is("tokens", tokens, (B, T), torch.int32)
+    _is("parent", parent, (B, T), torch.int32)
+    _is("coins", coins, (B, T), torch.float32)
+    _is("u", u, (B,), torch.float32)
+    if path is None:
+        path = torch.empty(B, max_path, dtype=torch.int32, device=dev)
+    else:
+        _is("path", path, (B, max_path), torch.int32)
+    if n_path is None:
+        n_path = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _is("n_path", n_path, (B,), torch.int32)
+    if next_token is None:
+        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _is("next_token", next_token, (B,), torch.int32)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    st = lib.gdr_verify_drafts(p.data_ptr(), None if q is None else q.data_ptr(),
+                               tokens.data_ptr(), parent.data_ptr(), coins.data_ptr(),
+                               u.data_ptr(), path.data_ptr(), n_path.data_ptr(),
+                               next_token.data_ptr(), B, T, V, _prob_rows("p", p),
+                               0 if q is None else _prob_rows("q", q), parent.stride(0),
+                               parent.stride(1), max_path,
+                               stream.cuda_stream, code)
+    _check(lib, st)
+    return path, n_path, next_token
+
+
+def gdr_commit_path(k, v, g, beta, path, n_path, h0=None, ht=None, stream=None, flags=0):
+    """The states after the accepted nodes of a draft (gdr_verify_drafts).
+
+    k, v, g, beta as gdr_forward_tree took them; path [B, P] and n_path [B] int32 on the GPU;
+    h0 [B, HV, dk, dv] f32 or None for zeros.  ``ht`` is allocated when not given; ``ht=h0``
+    updates in place.  Returns ht."""
+    lib = load_library()
+    B, T, HK, dk = k.shape
+    HV, dv = v.shape[2], v.shape[3]
+    dev = k.device
+    code = _dtype_code(k.dtype, "k and v")
+    _on_device(dev, ("k", k), ("v", v), ("g", g), ("beta", beta), ("path", path),
+               ("n_path", n_path), ("h0", h0), ("ht", ht))
+    _is("v", v, (B, T, HV, dv), k.dtype)
+    _is("beta", beta, (B, T, HV), torch.float32)
+    if g.dim() == 3:  # a scalar gate
+        flags |= GDR_FLAG_SCALAR_GATE
+        _is("g", g, (B, T, HV), torch.float32)
+    else:
+        _is("g", g, (B, T, HV, dk), torch.float32)
+    if path.dim() != 2:
+        raise ValueError("path must be [B, P]")
+    max_path = path.shape[1]
+    _is("path", path, (B, max_path), torch.int32)
+    _is("n_path", n_path, (B,), torch.int32)
+    if h0 is not None:
+        _is("h0", h0, (B, HV, dk, dv), torch.float32)
+    if ht is None:
+        ht = torch.empty(B, HV, dk, dv, dtype=torch.float32, device=dev)
+    elif ht is not h0:
+        _is("ht", ht, (B, HV, dk, dv), torch.float32)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    st = lib.gdr_commit_path(k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                             None if h0 is None else h0.data_ptr(), ht.data_ptr(),
+                             path.data_ptr(), n_path.data_ptr(), B, T, HK, HV, dk, dv, max_path,
+                             stream.cuda_stream, code, flags)
+    _check(lib, st)
+    return ht
+
+
+def gdr_state_cache(n_slots, HV, dk, dv, device="cuda"):
+    """An empty 8-bit cache of ``n_slots`` states: (cache int8 [n_slots, HV, dk, dv],
+    scale f32 [n_slots, HV, dk])."""
+    return (torch.zeros(n_slots, HV, dk, dv, dtype=torch.int8, device=device),
+            torch.zeros(n_slots, HV, dk, dtype=torch.float32, device=device))
+
+
+def _state_cache_shape(state, slots, cache, scale):
+    if cache.dim() != 4:
+        raise ValueError("cache must be [n_slots, HV, dk, dv]")
+    n_slots, HV, dk, dv = cache.shape
+    N = slots.shape[0] if slots.dim() == 1 else -1
+    _on_device(cache.device, ("cache", cache), ("scale", scale), ("slots", slots),
+               ("state", state))
+    _is("cache", cache, (n_slots, HV, dk, dv), torch.int8)
+    _is("scale", scale, (n_slots, HV, dk), torch.float32)
+    _is("slots", slots, (N,), torch.int32)
+    if state is not None:
+        _is("state", state, (N, HV, dk, dv), torch.float32)
+    return N, n_slots, HV, dk, dv
+
+
+def gdr_state_store(state, slots, cache, scale, stream=None):
+    """Quantises state [N, HV, dk, dv] f32 into the slots [N] (int32 on the GPU, all different;
+    below 0: not stored) of an 8-bit cache (gdr_state_cache)."""
+    lib = load_library()
+    N, n_slots, HV, dk, dv = _state_cache_shape(state, slots, cache, scale)
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    _check(lib, lib.gdr_state_store(state.data_ptr(), slots.data_ptr(), cache.data_ptr(),
+                                    scale.data_ptr(), N, n_slots, HV, dk, dv,
+                                    stream.cuda_stream))
+
+
+def gdr_state_load(cache, scale, slots, out=None, stream=None):
+    """The states [N, HV, dk, dv] f32 of the slots [N] of an 8-bit cache; zeros for a slot below
+    0.  ``out`` is allocated when not given.  Returns it."""
+    lib = load_library()
+    N, n_slots, HV, dk, dv = _state_cache_shape(out, slots, cache, scale)
+    if out is None:
+        out = torch.empty(N, HV, dk, dv, dtype=torch.float32, device=cache.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    _check(lib, lib.gdr_state_load(cache.data_ptr(), scale.data_ptr(), slots.data_ptr(),
+                                   out.data_ptr(), N, n_slots, HV, dk, dv, stream.cuda_stream))
     return out
 
 

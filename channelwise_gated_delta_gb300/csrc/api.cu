@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "gdr.h"
+#include "host_checks.h"
 
 // Device-wide error word: kernels that wait with a bounded spin set it
 // instead of hanging; gdr_device_check reads and clears it.
@@ -25,19 +26,12 @@ gdr_status cuda_fail(cudaError_t e) {
     return GDR_ERR_CUDA;
 }
 
-bool supported_dim(int d) { return d == 32 || d == 64 || d == 128; }
+using gdr::aligned16;
+using gdr::overlap;
+using gdr::Range;
+using gdr::range_of;
+using gdr::supported_dim;
 bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void *p, size_t bytes) {
-    return Range{(uintptr_t)p, (uintptr_t)p + bytes};
-}
-bool overlap(Range a, Range b) {
-    return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi;
-}
 
 // Validates pointers for BT token rows and NS state slots (alignment,
 // overlap); the shape checks common to every entry point.
@@ -375,7 +369,9 @@ const char *kKernelNames[gdr::kNumKernels] = {"gdr_decode_kernel", "gdr_chunk_pr
                                               "gdr_segment_init",  "gdr_segment_combine",
                                               "gdr_tree_tc",       "gdr_tree_path_kernel",
                                               "gdr_tree_gram_kernel", "gdr_tree_solve_kernel",
-                                              "gdr_chunk_scan_tc", "gdr_chunk_prep_tc"};
+                                              "gdr_chunk_scan_tc", "gdr_chunk_prep_tc",
+                                              "gdr_verify_kernel", "gdr_commit_kernel",
+                                              "gdr_state_store_kernel", "gdr_state_load_kernel"};
 
 }  // namespace
 

@@ -76,7 +76,11 @@ enum KernelId {
     kKernTreeSolve = 9,
     kKernChunkScanTc = 10,
     kKernChunkPrepTc = 11,
-    kNumKernels = 12
+    kKernVerify = 12,
+    kKernCommit = 13,
+    kKernStateStore = 14,
+    kKernStateLoad = 15,
+    kNumKernels = 16
 };
 // Called by the launchers around each launch; no-ops unless tracing is on.
 void trace_begin(int kernel, cudaStream_t stream);

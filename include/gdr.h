@@ -372,6 +372,142 @@ GDR_API gdr_status gdr_forward_tree(const void *q, const void *k, const void *v,
                                     size_t workspace_bytes, unsigned flags);
 
 /*
+ * The rest of a speculative step.  gdr_forward_tree gives the outputs of a
+ * tree of drafted tokens; the entries below decide which of them stand
+ * (gdr_verify_drafts), bring the states up to date with those
+ * (gdr_commit_path) and keep states at a quarter of their size
+ * (gdr_state_store / gdr_state_load).  Path, counts and slots are device
+ * memory and only read by kernels, so that the calls of a step follow one
+ * another on a stream, or in a CUDA graph, without the host learning what
+ * was accepted.  None of them needs a workspace or waits for the device.
+ *
+ * gdr_verify_drafts: verification of B trees of T nodes against the
+ * target's probabilities.  Node 0 of a tree is its root, the token already
+ * decided; node t > 0 is a drafted token, a child of node parent[t] < t.  A
+ * chain is the tree with parent[t] = t - 1.
+ *
+ *   p           [B][T] rows of V elements, ldp elements apart: row (b, t) is
+ *               the target's distribution of the token after node t
+ *   q           the draft's, rows ldq elements apart: row (b, t) is the
+ *               distribution that the children of node t were drawn from,
+ *               each by itself (rows of nodes without children are not
+ *               read).  NULL: the children were proposed, not drawn
+ *   tokens      int32 [B][T] token of each node (node 0's is not read)
+ *   parent      int32, of node t of tree b at parent[b * parent_sb + t * parent_st]
+ *               (a packed [B][T]: T and 1; one tree shape for the whole batch:
+ *               0 and 1).  Node 0's is not read
+ *   coins       float32 [B][T], one random number in [0, 1) per node (node
+ *               0's is not used)
+ *   u           float32 [B], one random number in [0, 1) per tree
+ *   path        int32 [B][max_path]: the accepted nodes from the root (path[0]
+ *               = 0) on, -1 behind them
+ *   n_path      int32 [B]: how many, 1 .. max_path
+ *   next_token  int32 [B]: the token after the last accepted node, -1 if that
+ *               node's row has no mass
+ *
+ * Rule.  Let P and Q be the rows of the node reached, an element that is NaN
+ * or negative counting as 0 and one above 1 as 1, and fix(x) = floor(2^40 x)
+ * a whole number.  The node's children are tried in the order of their
+ * index, unless the path holds max_path nodes.
+ *   With q: R = P at first.  Child x with coin c is accepted if R(x) > 0 and
+ *     c Q(x) < R(x).  A refusal makes R the residual r = max(R - Q, 0) over
+ *     its mass 2^-40 sum fix(r); if that sum is 0, R stays as it is.
+ *   Without q: M = 1 at first.  Child x is accepted if P(x) > 0, x was not
+ *     refused before and c M < P(x).  A refusal takes x's fix(P(x)) from
+ *     M (never below 0) and its weight from the row.
+ * Where no child is accepted the path ends and the next token is drawn from
+ * the weights w: the last residual r, or P without the refused tokens (all
+ * of P if nothing is left), or P where nothing was refused:  the lowest i
+ * with  sum_{j <= i} fix(w_j) > floor(m / 2^24 * sum_j fix(w_j)),  m =
+ * floor(2^24 u).  Every other operation is one float32 operation, rounded
+ * to nearest.  For p and q that sum to 1 the path and its next token are
+ * distributed as tokens drawn from p one after another.  Sums of whole
+ * numbers do not depend on their order: the result is the same for every
+ * split of the work, and so on every device.
+ *
+ * A node whose parent is not in [0, t - 1] or whose token is not in
+ * [0, V - 1] is never accepted and changes nothing.  A coin or u that is NaN
+ * counts as a refusal and as 0; u outside [0, 1) is clamped.  Supported:
+ * B >= 0, 1 <= T <= 512, 1 <= V <= 2^22, 1 <= max_path <= T, ldp >= V,
+ * ldq >= V, parent_sb and parent_st >= 0, prob_dtype GDR_F32 or GDR_BF16 (p
+ * and q both); p and q 16-byte aligned, everything else 4-byte.  Errors: GDR_ERR_UNSUPPORTED for T > 512,
+ * V > 2^22 or another dtype, GDR_ERR_SHAPE for the other limits, the rest as
+ * gdr_forward_ex.
+ * Passage: none in the pages ("Support TreeUpdateSolve kernel",
+ * trymirai/uzu PR #576, computes a draft tree's outputs; what a decoder does
+ * with them is not in it).
+ */
+GDR_API gdr_status gdr_verify_drafts(const void *p, const void *q, const int *tokens,
+                                     const int *parent, const float *coins, const float *u,
+                                     int *path, int *n_path, int *next_token, int B, int T, int V,
+                                     long long ldp, long long ldq, long long parent_sb,
+                                     long long parent_st, int max_path, void *stream,
+                                     int prob_dtype);
+
+/*
+ * The states after the accepted nodes: sequence b starts from h0[b] (zeros
+ * if NULL) and takes the recurrence's step (decay, predict, update; no
+ * output) for its nodes path[b][0], path[b][1], ..., path[b][n_path[b] - 1]
+ * in this order.
+ *
+ *   k, v, g, beta  layouts as in gdr_forward, T rows per sequence: those that
+ *                  gdr_forward_tree (or gdr_forward) was given
+ *   h0, ht         [B][HV][dk][dv] float32; ht == h0 updates in place
+ *   path           int32 [B][max_path], n_path int32 [B], device memory (as
+ *                  gdr_verify_drafts writes them)
+ *
+ * A sequence's path ends before the first entry outside [0, T - 1]; n_path
+ * below 0 counts as 0, above max_path as max_path.  With no node ht = h0.
+ * flags: GDR_FLAG_SCALAR_GATE or 0.  The state stays float32 throughout and
+ * is read and written once, whatever the path's length.  Supported: B >= 0,
+ * T >= 1, max_path >= 0, HK, HV, dk, dv as in gdr_forward.  Errors as
+ * gdr_forward_ex (GDR_ERR_UNSUPPORTED for other flags; path and n_path
+ * 4-byte aligned).
+ * Passage: "Reorder channelwise gated delta rule chunked hot loops for
+ * autovectorization" (pytorch/executorch PR #21021), first commit summary:
+ * the token recurrence, without its output sweep.
+ */
+GDR_API gdr_status gdr_commit_path(const void *k, const void *v, const float *g, const float *beta,
+                                   const float *h0, float *ht, const int *path, const int *n_path,
+                                   int B, int T, int HK, int HV, int dk, int dv, int max_path,
+                                   void *stream, int kv_dtype, unsigned flags);
+
+/*
+ * An 8-bit cache of states, by slots: states that wait (a shared prefix, a
+ * paused sequence) at 1/4 of their size.  A row of a state (one key channel,
+ * dv values) is held as whole numbers in [-127, 127] and one scale.
+ *
+ *   state  [N][HV][dk][dv]      float32
+ *   slots  int32 [N]            device memory: the slot of each state
+ *   cache  int8 [n_slots][HV][dk][dv],  scale float32 [n_slots][HV][dk]
+ *
+ * gdr_state_store: a = the largest magnitude of the row; scale = a * (1 / 127)
+ * and code = x * (127 * (1 / a)) rounded to the nearest whole number (ties to
+ * even), each a float32 operation rounded to nearest.  A row with a <= 1e-30 is stored as
+ * zeros with scale 0.  A row that holds an infinity or a NaN is stored as
+ * zeros with scale NaN, so that it comes back as NaN and not as plausible
+ * numbers.  A state whose slot is outside [0, n_slots - 1] is not stored;
+ * the slots of one call must differ from each other.
+ * gdr_state_load: state = code * scale; a state whose slot is outside
+ * [0, n_slots - 1] is set to zero (a new sequence); a slot may be loaded
+ * more than once.
+ * The error of a value is at most half its row's scale, 1/254 of the row's
+ * largest magnitude.  The rows are scaled one by one because each key
+ * channel decays at its own rate; the states that the recurrence runs on
+ * stay float32.
+ *
+ * Supported: N >= 0, n_slots >= 0, HV >= 1, dk and dv in {32, 64, 128}.
+ * state and cache 16-byte aligned, slots and scale 4-byte.  Errors as
+ * gdr_forward_ex.  Passage: none in the pages.
+ */
+GDR_API gdr_status gdr_state_store(const float *state, const int *slots, signed char *cache,
+                                   float *scale, int N, int n_slots, int HV, int dk, int dv,
+                                   void *stream);
+GDR_API gdr_status gdr_state_load(const signed char *cache, const float *scale, const int *slots,
+                                  float *state, int N, int n_slots, int HV, int dk, int dv,
+                                  void *stream);
+
+/*
  * Passage: none in the pages (error reporting of the bounded waits).
  * Waits for `stream`, then reads and clears the library's device error word
  * on the current device.  Returns GDR_ERR_TIMEOUT if a kernel gave up on a
