@@ -7,178 +7,469 @@
 // is summed in whole numbers of 2^-40, so that every order of summation
 // gives the same sums; each other operation is one float32 operation,
 // written with its rounding so that no contraction changes it.
+//
+// Only the last node's rows are read whole (and those of a node that was
+// passed after refusals with q): the walk itself needs two elements per
+// drafted token, which all are gathered at once.  What bounds the call is
+// the latency of that chain -- tokens and parents, the gathered elements,
+// the rows, the totals, the token's neighbourhood -- and for large batches
+// the bandwidth of the rows.  A tree is therefore one cluster of CTAs, each
+// of which walks the tree for itself (the same numbers, so the same walk)
+// and sums its part of the rows; the totals meet in shared memory across
+// the cluster, and the CTA in whose part the goal lies finds the token.
 #include <stdint.h>
 
 #include "common.cuh"
 #include "gdr.h"
 #include "host_checks.h"
+#include "sm100_ptx.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kMaxNodes = 512;
 constexpr int kMaxVocab = 1 << 22;  // 2^22 weights of at most 2^40 each: sums below 2^63
-constexpr int kThreads = 512;
-constexpr float kUnit = 1099511627776.f;         // 2^40
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;  // the portable limit
+constexpr int kAhead = 4;       // 16-byte loads a lane has in flight per row
+constexpr float kUnit = 1099511627776.f;            // 2^40
 constexpr float kUnitInv = 9.094947017729282e-13f;  // 2^-40
 constexpr int kUBits = 24;
 
 // A probability as it counts: NaN and negative 0, above 1 at most 1.
-template <typename Tp>
-__device__ __forceinline__ float probability(Tp x) {
-    return fminf(fmaxf(to_f32(x), 0.f), 1.f);  // fmaxf(NaN, 0) = 0
+__device__ __forceinline__ float probability(float x) {
+    return fminf(fmaxf(x, 0.f), 1.f);  // fmaxf(NaN, 0) = 0
 }
 __device__ __forceinline__ long long fix(float x) { return __float2ll_rz(__fmul_rn(x, kUnit)); }
 __device__ __forceinline__ float mass_of(long long sum) {
     return __fmul_rn(__ll2float_rn(sum), kUnitInv);
 }
 
-struct Residual {
-    float scaled;  // R: what the next child is tried against
-    float weight;  // r of the last refusal that left something (P before any)
-};
-// An element of the rows after n refusals with q; norm[s]: mass of residual
-// s, 0 where it had none.
-__device__ __forceinline__ Residual residual(float P, float Q, const float *norm, int n) {
-    Residual x{P, P};
+// An element's weight after n refusals with q: the residual of the last one
+// that left something (P before any); norm[s] is the mass of residual s, 0
+// where it had none.
+__device__ __forceinline__ float residual(float P, float Q, const float *norm, int n) {
+    float weight = P, scaled = P;
     for (int s = 0; s < n; ++s) {
         if (norm[s] == 0.f) continue;
-        x.weight = fmaxf(__fsub_rn(x.scaled, Q), 0.f);
-        x.scaled = __fdiv_rn(x.weight, norm[s]);
+        weight = fmaxf(__fsub_rn(scaled, Q), 0.f);
+        if (s + 1 < n) scaled = __fdiv_rn(weight, norm[s]);
     }
+    return weight;
+}
+
+// ---- a row of V elements, addressed by j = i + shift, shift being the
+// elements between the 16-byte boundary at or before the row and its start:
+// vectors of VEC elements at multiples of VEC are aligned for every row.
+template <typename Tp>
+struct Vec {
+    static constexpr int N = 16 / (int)sizeof(Tp);
+};
+template <typename Tp>
+__device__ __forceinline__ int row_shift(const Tp *row) {
+    return (int)(((uintptr_t)row & 15u) / sizeof(Tp));
+}
+__device__ __forceinline__ void unpack(uint4 r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.x);
+    x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z);
+    x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(uint4 r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+
+// Elements i0 .. i0 + VEC - 1 of a row one by one, 0 outside of it: for the
+// ends of a row, and for rows of q that do not lie to 16 bytes as p's do.
+template <typename Tp>
+__device__ __forceinline__ uint4 load_elements(const Tp *row, int i0, int V) {
+    constexpr int N = Vec<Tp>::N;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int i = i0 + e;
+        if (i >= 0 && i < V) w[e * 4 / N] |= bits_of(row[i]) << (N == 8 ? 16 * (e & 1) : 0);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename Tp>
+__device__ __forceinline__ uint4 load_vec(const Tp *row, int i0) {
+    return __ldg(reinterpret_cast<const uint4 *>(row + i0));
+}
+
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
 }
 
-template <typename Tp>
-__global__ void __launch_bounds__(kThreads)
+// ---- the cluster
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores x to the same variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote(long long *var, int rank, long long x) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "st.shared::cluster.b64 [a], %2;\n\t}" ::"r"(sm100::smem_u32(var)),
+        "r"(rank), "l"(x)
+        : "memory");
+}
+
+template <typename Tp, bool HAS_Q>
+__global__ void __launch_bounds__(kThreads, 4)
     gdr_verify_kernel(const Tp *__restrict__ p, const Tp *__restrict__ q,
                       const int *__restrict__ tokens, const int *__restrict__ parent,
                       const float *__restrict__ coins, const float *__restrict__ u,
                       int *__restrict__ path, int *__restrict__ n_path,
                       int *__restrict__ next_token, int T, int V, long long ldp, long long ldq,
-                      long long parent_sb, long long parent_st, int max_path) {
+                      long long parent_sb, long long parent_st, int max_path, int cluster) {
+    constexpr int N = Vec<Tp>::N;
+    constexpr int kWide = 32 * N;  // elements of a warp's load: a unit of the row
     __shared__ int s_parent[kMaxNodes], s_token[kMaxNodes];
     __shared__ float s_coin[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
     __shared__ float s_norm[kMaxNodes];   // with q: the mass of each residual
-    __shared__ int s_refused[kMaxNodes];  // without q: the tokens refused
-    __shared__ long long s_sum[kThreads];
-    __shared__ int s_here, s_tried, s_out, s_state;
-    const int b = blockIdx.x, tid = threadIdx.x;
+    __shared__ int s_refused[kMaxNodes];  // without q: the nodes refused
+    __shared__ long long s_warp[kWarps];
+    __shared__ long long s_total[2][kMaxCluster];
+    __shared__ int s_here, s_out, s_more, s_summed;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / cluster, rank = blockIdx.x - b * cluster;
+    cluster_arrive();  // (1) this CTA runs: its shared memory may be written
 
     for (int t = tid; t < T; t += kThreads) {
         const size_t at = (size_t)b * T + t;
-        const int par = t > 0 ? parent[b * parent_sb + t * parent_st] : -1, tok = t > 0 ? tokens[at] : -1;
+        int par = -1, tok = -1;
+        if (t > 0) {
+            par = parent[b * parent_sb + t * parent_st];
+            tok = tokens[at];
+        }
+        const float coin = coins[at];
         const bool ok = par >= 0 && par < t && tok >= 0 && tok < V;
         const size_t row = (size_t)b * T + (ok ? par : 0);
+        s_p[t] = ok ? probability(to_f32(p[row * ldp + tok])) : 0.f;
+        s_q[t] = ok && HAS_Q ? probability(to_f32(q[row * ldq + tok])) : 0.f;
         s_parent[t] = ok ? par : -1;
         s_token[t] = tok;
-        s_coin[t] = coins[at];
-        s_p[t] = ok ? probability(p[row * ldp + tok]) : 0.f;
-        s_q[t] = ok && q ? probability(q[row * ldq + tok]) : 0.f;
+        s_coin[t] = coin;
     }
-    if (tid == 0) {
-        s_here = 0;   // the node reached
-        s_tried = 0;  // nodes up to this one have been tried
-        s_out = 0;    // refusals at s_here
-        path[(size_t)b * max_path] = 0;
-    }
+    const float uu = u[b];
     __syncthreads();
 
-    // sums the weights of this thread's part of the rows of the node reached
-    const int per = (V + kThreads - 1) / kThreads;
-    const int lo = min(V, tid * per), hi = min(V, lo + per);
-    auto weight = [&](int i, int n, bool all) -> float {
-        const size_t row = (size_t)b * T + s_here;
-        const float P = probability(p[row * ldp + i]);
-        if (q) return residual(P, probability(q[row * ldq + i]), s_norm, n).weight;
-        if (!all)
-            for (int s = 0; s < n; ++s)
-                if (s_refused[s] == i) return 0.f;
-        return P;
+    // ---- this warp's part of the rows of the node reached
+    const Tp *prow = nullptr, *qrow = nullptr;
+    int shift = 0, u0 = 0, u1 = 0, c0 = 0, per_warp = 0, units = 0;
+    int f0 = 0, f1 = 0;  // the units whose vectors are aligned and inside the row
+    auto take_rows = [&](int node) {
+        const size_t row = (size_t)b * T + node;
+        prow = p + row * ldp;
+        shift = row_shift(prow);
+        f0 = shift > 0 ? 1 : 0;
+        f1 = (V + shift) / kWide;
+        if (HAS_Q) {
+            qrow = q + row * ldq;
+            if (row_shift(qrow) != shift) f1 = f0;
+        }
+        units = (V + shift + kWide - 1) / kWide;
+        const int per_cta = (units + cluster - 1) / cluster;
+        per_warp = (per_cta + kWarps - 1) / kWarps;
+        c0 = rank * per_cta;  // this CTA's units: c0 .. min(c0 + per_cta, units) - 1
+        const int c1 = min(c0 + per_cta, units);
+        u0 = min(c0 + warp * per_warp, c1);
+        u1 = min(u0 + per_warp, c1);
     };
-    auto sum_row = [&](int n, bool all) -> long long {  // exclusive sums in s_sum, total returned
+    // weights of the elements of a lane's vector; refusals without q are taken off elsewhere
+    auto weights = [&](uint4 pv, uint4 qv, int n, float (&w)[N]) {
+        unpack(pv, w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[e] = probability(w[e]);
+        if (HAS_Q && n > 0) {
+            float x[N];
+            unpack(qv, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = probability(x[e]);
+            if (n == 1 && s_norm[0] != 0.f) {  // nearly every row that is read whole
+#pragma unroll
+                for (int e = 0; e < N; ++e) w[e] = fmaxf(__fsub_rn(w[e], x[e]), 0.f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) w[e] = residual(w[e], x[e], s_norm, n);
+            }
+        }
+    };
+    // the weights of this lane's elements of a unit
+    auto unit_weights = [&](int unit, int n, float (&w)[N]) {
+        const int i0 = unit * kWide + lane * N - shift;
+        uint4 pv, qv = make_uint4(0u, 0u, 0u, 0u);
+        if (unit >= f0 && unit < f1) {
+            pv = load_vec(prow, i0);
+            if (HAS_Q && n > 0) qv = load_vec(qrow, i0);
+        } else {
+            pv = load_elements(prow, i0, V);
+            if (HAS_Q && n > 0) qv = load_elements(qrow, i0, V);
+        }
+        weights(pv, qv, n, w);
+    };
+    // mass of units lo .. hi - 1 after n refusals, in every lane of the warp
+    auto mass = [&](int lo, int hi, int n) -> long long {
         long long part = 0;
-        for (int i = lo; i < hi; ++i) part += fix(weight(i, n, all));
-        s_sum[tid] = part;
+        for (int at = lo; at < hi; at += kAhead) {
+            uint4 pv[kAhead], qv[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool whole = at + k < hi && at + k >= f0 && at + k < f1;
+                const int i0 = (at + k) * kWide + lane * N - shift;
+                pv[k] = whole ? load_vec(prow, i0) : make_uint4(0u, 0u, 0u, 0u);
+                qv[k] = HAS_Q && n > 0 && whole ? load_vec(qrow, i0) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (at < f0 || min(at + kAhead, hi) > f1) {
+                for (int k = 0; k < kAhead; ++k) {
+                    if (at + k >= hi || (at + k >= f0 && at + k < f1)) continue;
+                    float w[N];
+                    unit_weights(at + k, n, w);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) part += fix(w[e]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                float w[N];
+                weights(pv[k], qv[k], n, w);
+#pragma unroll
+                for (int e = 0; e < N; ++e) part += fix(w[e]);
+            }
+        }
+        if (!HAS_Q)
+            for (int s = lane; s < n; s += 32) {
+                const int unit = (s_token[s_refused[s]] + shift) / kWide;
+                if (unit >= lo && unit < hi) part -= fix(s_p[s_refused[s]]);
+            }
+        return warp_sum(part);
+    };
+    int round = 0;
+    // total mass of the node's rows after n refusals; each warp's in s_warp,
+    // each CTA's in s_total[round & 1]
+    auto total_mass = [&](int n) -> long long {
+        const long long mine = mass(u0, u1, n);
+        if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
-        long long total = 0;
-        for (int i = 0; i < kThreads; ++i) total += s_sum[i];
-        __syncthreads();
-        return total;
+        ++round;
+        long long *totals = s_total[round & 1];
+        if (round == 1) cluster_wait();  // (1)
+        if (warp == 0) {
+            const long long all = warp_sum(lane < kWarps ? s_warp[lane] : 0);
+            if (lane < cluster) store_remote(totals + rank, lane, all);
+            __syncwarp();
+        }
+        cluster_arrive();
+        cluster_wait();
+        long long sum = 0;
+        for (int r = 0; r < cluster; ++r) sum += totals[r];
+        return sum;
     };
 
-    int n = 1;  // thread 0: nodes on the path
+    // ---- the walk, by warp 0 of each CTA: until the path ends, or with q
+    // until a refusal's mass is wanted
+    int here = 0, tried = 0, out = 0, n = 1;
+    long long total = 0;
+    bool summed = false;  // total is that of the weights after `out` refusals at `here`
     long long left = (long long)kUnit;
+    const bool writer = rank == 0 && tid == 0;
+    int *my_path = path + (size_t)b * max_path;
+    if (writer) my_path[0] = 0;
     while (true) {
-        if (tid == 0) {
-            // tries children until one is refused with q (state 1) or the path ends (state 0)
-            s_state = 0;
-            int t = s_tried;
+        if (warp == 0) {
+            bool more = false;
             while (n < max_path) {
-                for (++t; t < T && s_parent[t] != s_here; ++t) {
+                // the next child of `here` behind node `tried`
+                int t = T;
+                for (int base = (tried + 1) & ~31; base < T; base += 32) {
+                    const int at = base + lane;
+                    const unsigned hit = __ballot_sync(
+                        0xffffffffu, at > tried && at < T && s_parent[min(at, T - 1)] == here);
+                    if (hit) {
+                        t = base + __ffs(hit) - 1;
+                        break;
+                    }
                 }
                 if (t >= T) break;
+                tried = t;
                 float a, bar;
-                if (q) {
-                    a = residual(s_p[t], s_q[t], s_norm, s_out).scaled;
+                if (HAS_Q) {
+                    a = s_p[t];
+                    for (int s = 0; s < out; ++s)
+                        if (s_norm[s] != 0.f)
+                            a = __fdiv_rn(fmaxf(__fsub_rn(a, s_q[t]), 0.f), s_norm[s]);
                     bar = __fmul_rn(s_coin[t], s_q[t]);
                 } else {
-                    a = s_p[t];
-                    for (int s = 0; s < s_out; ++s)
-                        if (s_refused[s] == s_token[t]) a = 0.f;
+                    bool again = false;
+                    for (int s = lane; s < out; s += 32)
+                        again = again || s_token[s_refused[s]] == s_token[t];
+                    a = __any_sync(0xffffffffu, again) ? 0.f : s_p[t];
                     bar = __fmul_rn(s_coin[t], mass_of(left));
                 }
                 if (a > 0.f && bar < a) {
-                    s_here = t;
-                    s_out = 0;
+                    here = t;
+                    out = 0;
+                    summed = false;
                     left = (long long)kUnit;
-                    path[(size_t)b * max_path + n++] = t;
-                } else if (q) {
-                    s_norm[s_out++] = 1.f;  // its mass follows
-                    s_state = 1;
+                    if (writer) my_path[n] = t;
+                    ++n;
+                } else if (HAS_Q) {
+                    if (lane == 0) s_norm[out] = 1.f;  // its mass follows
+                    ++out;
+                    more = true;
                     break;
-                } else {
+                } else if (a > 0.f) {  // what has no mass need not be taken off
                     left = max(left - fix(a), 0ll);
-                    s_refused[s_out++] = s_token[t];
+                    __syncwarp();
+                    if (lane == 0) s_refused[out] = t;
+                    ++out;
+                    __syncwarp();
                 }
             }
-            s_tried = t;
-        }
-        __syncthreads();
-        if (s_state == 0) break;
-        const long long total = sum_row(s_out, false);
-        if (tid == 0) s_norm[s_out - 1] = mass_of(total);
-        __syncthreads();
-    }
-
-    long long total = sum_row(s_out, false);
-    bool all = false;
-    if (total == 0 && !q && s_out > 0) {  // nothing left: the row as it was
-        all = true;
-        total = sum_row(s_out, true);
-    }
-    if (tid == 0) {
-        for (int i = n; i < max_path; ++i) path[(size_t)b * max_path + i] = -1;
-        n_path[b] = n;
-        if (total == 0) next_token[b] = -1;
-    }
-    if (total == 0) return;
-    const float top = 1.f - 1.f / (1 << kUBits);
-    const long long m =
-        (long long)__fmul_rn(fminf(fmaxf(u[b], 0.f), top), (float)(1 << kUBits));
-    const long long low = (1 << kUBits) - 1;
-    const long long goal = (total >> kUBits) * m + (((total & low) * m) >> kUBits);
-    long long run = 0;
-    for (int i = 0; i < tid; ++i) run += s_sum[i];
-    if (run <= goal && goal < run + s_sum[tid]) {
-        for (int i = lo; i < hi; ++i) {
-            run += fix(weight(i, s_out, all));
-            if (run > goal) {
-                next_token[b] = i;
-                break;
+            if (lane == 0) {
+                s_here = here;
+                s_out = out;
+                s_more = more;
+                s_summed = summed;
             }
         }
+        __syncthreads();
+        here = s_here;
+        out = s_out;
+        summed = s_summed;
+        if (!HAS_Q || !s_more) break;
+        take_rows(here);
+        total = total_mass(out);
+        summed = total > 0;  // without mass the weights stay those of before
+        if (tid == 0) s_norm[out - 1] = mass_of(total);
+        __syncthreads();
     }
+    if (writer) {
+        for (int i = n; i < max_path; ++i) my_path[i] = -1;
+        n_path[b] = n;
+    }
+
+    // ---- the next token
+    if (!HAS_Q || !summed) {
+        take_rows(here);
+        total = total_mass(out);
+    }
+    if (!HAS_Q && total == 0 && out > 0) {  // nothing left: the row as it was
+        out = 0;
+        total = total_mass(0);
+    }
+    if (total == 0) {
+        if (writer) next_token[b] = -1;
+        return;
+    }
+    const float top = 1.f - 1.f / (1 << kUBits);
+    const long long m = (long long)__fmul_rn(fminf(fmaxf(uu, 0.f), top), (float)(1 << kUBits));
+    const long long low = (1 << kUBits) - 1;
+    long long goal = (total >> kUBits) * m + (((total & low) * m) >> kUBits);  // floor(total m / 2^24)
+    const long long *totals = s_total[round & 1];
+    for (int r = 0; r < rank; ++r) goal -= totals[r];
+    if (goal < 0 || goal >= totals[rank]) return;
+    // the warp, then an eighth of its units, then the element
+    int w = 0;
+    for (; goal >= s_warp[w]; ++w) goal -= s_warp[w];
+    const int per_cta = (units + cluster - 1) / cluster, c1 = min(c0 + per_cta, units);
+    const int w0 = min(c0 + w * per_warp, c1), w1 = min(w0 + per_warp, c1);
+    const int step = (w1 - w0 + kWarps - 1) / kWarps;
+    const int m0 = min(w0 + warp * step, w1), m1 = min(m0 + step, w1);
+    __syncthreads();
+    const long long mine = mass(m0, m1, out);
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    w = 0;
+    for (; goal >= s_warp[w]; ++w) goal -= s_warp[w];
+    if (w != warp) return;
+    for (int at = m0; at < m1; ++at) {
+        const int j0 = at * kWide + lane * N;
+        float x[N];
+        unit_weights(at, out, x);
+        if (!HAS_Q)
+            for (int s = 0; s < out; ++s) {
+                const int e = s_token[s_refused[s]] + shift - j0;
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (k == e) x[k] = 0.f;
+            }
+        long long own = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) own += fix(x[e]);
+        long long upto = own;  // of the lanes up to this one
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        if (upto - own <= goal && goal < upto) {
+            long long run = upto - own;
+            int found = 0;
+#pragma unroll
+            for (int e = N - 1; e >= 0; --e) {  // the first element whose running sum is above
+                long long sum = run;
+#pragma unroll
+                for (int k = 0; k <= e; ++k) sum += fix(x[k]);
+                if (sum > goal) found = e;
+            }
+            next_token[b] = j0 + found - shift;
+        }
+        const long long all = __shfl_sync(0xffffffffu, upto, 31);
+        if (goal < all) return;
+        goal -= all;
+    }
+}
+
+// CTAs per tree: a power of two up to the cluster limit, doubled while all
+// the trees' CTAs would leave the device's slots (4 a SM) empty and each would keep at
+// least 1024 elements.
+int cluster_size(int B, int V, int sms) {
+    int c = 1;
+    while (c < kMaxCluster && (long long)B * c < 4LL * sms && V / (2 * c) >= 1024) c *= 2;
+    return c;
+}
+
+template <typename Tp, bool HAS_Q>
+cudaError_t launch_q(const void *p, const void *q, const int *tokens, const int *parent,
+                     const float *coins, const float *u, int *path, int *n_path, int *next_token,
+                     int B, int T, int V, long long ldp, long long ldq, long long parent_sb,
+                     long long parent_st, int max_path, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int c = cluster_size(B, V, sms);
+    if ((long long)B * c > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(B * c));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    trace_begin(kKernVerify, stream);
+    e = cudaLaunchKernelEx(&cfg, gdr_verify_kernel<Tp, HAS_Q>, static_cast<const Tp *>(p),
+                           static_cast<const Tp *>(q), tokens, parent, coins, u, path, n_path,
+                           next_token, T, V, ldp, ldq, parent_sb, parent_st, max_path, c);
+    trace_end(kKernVerify, stream);
+    return e;
 }
 
 template <typename Tp>
@@ -186,12 +477,10 @@ cudaError_t launch(const void *p, const void *q, const int *tokens, const int *p
                    const float *coins, const float *u, int *path, int *n_path, int *next_token,
                    int B, int T, int V, long long ldp, long long ldq, long long parent_sb,
                    long long parent_st, int max_path, cudaStream_t stream) {
-    trace_begin(kKernVerify, stream);
-    gdr_verify_kernel<Tp><<<B, kThreads, 0, stream>>>(
-        static_cast<const Tp *>(p), static_cast<const Tp *>(q), tokens, parent, coins, u, path,
-        n_path, next_token, T, V, ldp, ldq, parent_sb, parent_st, max_path);
-    trace_end(kKernVerify, stream);
-    return cudaGetLastError();
+    return q ? launch_q<Tp, true>(p, q, tokens, parent, coins, u, path, n_path, next_token, B, T,
+                                  V, ldp, ldq, parent_sb, parent_st, max_path, stream)
+             : launch_q<Tp, false>(p, q, tokens, parent, coins, u, path, n_path, next_token, B, T,
+                                   V, ldp, ldq, parent_sb, parent_st, max_path, stream);
 }
 
 // Whether `rows` rows `ld` apart are addressable (element offsets below 2^58).
