@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "gdr.h"
 #include "host_checks.h"
+#include "sm100_ptx.cuh"
 
 namespace gdr {
 namespace {
@@ -160,6 +161,395 @@ __global__ void __launch_bounds__(2 * BV, BV == 64 ? 4 : 8)
     }
 }
 
+// ---- dk = dv = 128 and many heads: persistent, the 64 KB states by bulk copies.
+//
+// One CTA per SM walks heads blockIdx.x, + gridDim.x, ...  The kernel above
+// waits for a chain of loads (path length, path, k / g / v of its nodes)
+// before a head's first step and has nothing else to do meanwhile.  Here a
+// head belongs to one of two groups of four warps in turn; a producer warp
+// per group brings its heads' nodes (k, exp(g), v, beta as float32, four
+// nodes a slot, the next four's loads in flight) and states (three 64 KB
+// buffers, which the groups share in the order of the heads).  A group copies
+// its state into registers, frees the buffer at once and stores from the
+// registers, so that all three buffers are reads ahead.
+//
+// Warp w of a group owns columns 32 w .. + 31: lane (cq = lane % 8, rg = lane
+// / 8) holds columns 4 cq .. + 3 of the rows 4 rg + 16 m .. + 3 (m < 8) as
+// pairs of rows, so that k and a are pairs as they lie in shared memory.
+constexpr int kD = 128;
+constexpr int kBufs = 3;
+constexpr int kSlots = 2;
+constexpr int kSlotNodes = 4;
+constexpr int kGroups = 2;
+constexpr int kGroupWarps = 4;
+constexpr int kHalf = kSlotNodes / 2;  // nodes of a slot per producer warp
+// Two warpgroups of states and one of producers: registers move between
+// warpgroups.  384 threads are launched with 168 registers each, 64512 in
+// all: 2 x 128 x 200 + 128 x 104.
+constexpr int kBulkThreads = (kGroups + 1) * kGroupWarps * 32;
+constexpr int kStateRegs = 200, kProducerRegs = 104;
+constexpr uint32_t kStateBytes = kD * kD * 4;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+
+static_assert(kBufs == 3 && kGroups == 2, "the order of the waits goes by these");
+
+struct Slot {
+    float k[kSlotNodes][kD], a[kSlotNodes][kD], v[kSlotNodes][kD];
+    float beta[kSlotNodes];
+    int count, last, pad[2];
+};
+struct BulkShared {
+    float state[kBufs][kD * kD];
+    Slot slot[kGroups][kSlots];
+    uint64_t state_full[kBufs], state_empty[kBufs];
+    uint64_t full[kGroups][kSlots], empty[kGroups][kSlots];
+};
+
+// Four elements of a row as they lie in memory.
+template <typename Tin>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 x;
+    __device__ __forceinline__ void load(const float *p) { x = load4(p); }
+    __device__ __forceinline__ float4 f32() const { return x; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 x;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        x = *reinterpret_cast<const uint2 *>(p);
+    }
+    __device__ __forceinline__ float4 f32() const {
+        return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                           __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+    }
+};
+
+// Whether the phase with that parity has completed; returns at once.
+__device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sm100::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// A wait of a whole warp, with the same answer in every lane.  The waits here
+// are short and many, so the warp polls rather than sleeps; it looks at
+// the clock every 1024 polls.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = sm100::global_timer_ns();
+    for (int n = 0;; ++n) {
+        if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity))) return true;
+        if ((n & 1023) == 1023 &&
+            __any_sync(0xffffffffu, sm100::global_timer_ns() - t0 > kWaitNs))
+            return false;
+    }
+}
+
+template <typename Tin, bool GS>
+__global__ void __launch_bounds__(kBulkThreads, 1)
+    gdr_commit_bulk_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v,
+                           const float *__restrict__ g, const float *__restrict__ beta,
+                           const float *h0, float *ht, const int *__restrict__ path,
+                           const int *__restrict__ n_path, int T, int HK, int HV, int max_path,
+                           int nheads, int *dev_error) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    BulkShared &sh = *reinterpret_cast<BulkShared *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < kBufs; ++i) {
+            sm100::mbar_init(&sh.state_full[i], 1);
+            sm100::mbar_init(&sh.state_empty[i], kGroupWarps);
+        }
+        for (int i = 0; i < kGroups; ++i)
+            for (int j = 0; j < kSlots; ++j) {
+                sm100::mbar_init(&sh.full[i][j], kSlotNodes / kHalf);
+                sm100::mbar_init(&sh.empty[i][j], kGroupWarps);
+            }
+        sm100::fence_mbar_init();
+    }
+    __syncthreads();
+    // the CTA's heads: number i is head blockIdx.x + i gridDim.x, in buffer i % kBufs
+    const int my = (nheads - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;
+    bool ok = true;
+
+    if (warp >= kGroups * kGroupWarps) {
+        // ---- producer of group grp: heads grp, grp + 2, ...
+        // Two warps per group: nodes 2 half, 2 half + 1 of each slot; the
+        // first also asks for the states and writes the slot's count.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        const int grp = (warp - kGroups * kGroupWarps) & 1, half = (warp - kGroups * kGroupWarps) >> 1;
+        int next_state = grp;  // the group's next head whose state has not been asked for
+        // Asks for the states of heads up to `upto`, waiting for their buffers,
+        // and up to `may` where that needs no wait.  A buffer's barriers tell
+        // a phase only from the one before it, so head i's state may be asked for only once
+        // head i - 6, the user of its buffer two uses ago, is known to have been
+        // read: head i - 6 is this group's, every head takes at least one
+        // slot, and a slot is filled again only after the group has
+        // worked through it.  Before the wait for the slot of a head's
+        // nodes that is known for the head itself, after it for the next one.
+        auto states = [&](int upto, int may) {
+            while (half == 0 && ok && h0 && next_state < my && next_state <= may) {
+                const int buf = next_state % kBufs, use = next_state / kBufs;
+                if (use > 0) {
+                    const uint32_t parity = (uint32_t)(use - 1) & 1u;
+                    if (next_state <= upto)
+                        ok = warp_wait(&sh.state_empty[buf], parity);
+                    else if (!__all_sync(0xffffffffu, test_wait(&sh.state_empty[buf], parity)))
+                        break;
+                }
+                if (ok && lane == 0) {
+                    sm100::mbar_arrive_expect_tx(&sh.state_full[buf], kStateBytes);
+                    const size_t head = (size_t)blockIdx.x + (size_t)next_state * gridDim.x;
+                    sm100::bulk_load_1d(sh.state[buf], h0 + head * kD * kD, kStateBytes,
+                                        &sh.state_full[buf]);
+                }
+                __syncwarp();
+                if (ok) next_state += kGroups;
+            }
+        };
+        // sequence, value head and key head of the head whose nodes are loaded;
+        // the group's heads are kGroups gridDim.x apart
+        const int step_b = kGroups * (int)gridDim.x / HV, step_h = kGroups * (int)gridDim.x % HV;
+        const int first = blockIdx.x + grp * gridDim.x;
+        const int per_key = HV / HK;
+        int b = first / HV, hv = first % HV, hk = hv / per_key;
+        // a head's path: its length and entry `from + lane` (of sequence bb)
+        auto entries = [&](int bb, int from, int &len) -> int {
+            len = n_path[bb];  // held to max_path where it is used: no wait for it here
+            return from + lane < max_path ? path[(size_t)bb * max_path + from + lane] : -1;
+        };
+        struct Nodes {
+            Raw4<Tin> k[kHalf], v[kHalf];
+            float4 g[kHalf];
+            float beta, gate;  // of node `lane`
+            int count, last;
+        };
+        int head_i = grp, at = 0, n = 0, n_next = 0, entry = -1, entry_next = -1;
+        if (head_i < my) entry = entries(b, 0, n);
+        states(grp, grp + kGroups);
+        auto next_b = [&]() { return b + step_b + (hv + step_h >= HV ? 1 : 0); };
+        if (head_i + kGroups < my) entry_next = entries(next_b(), 0, n_next);
+        // loads this warp's nodes of at .. at + 3 of head head_i, up to the path's end
+        auto load = [&](Nodes &x) {
+            n = min(n, max_path);
+            const unsigned good =
+                __ballot_sync(0xffffffffu, (at & ~31) + lane < n && entry >= 0 && entry < T);
+            x.count = min(kSlotNodes, __ffs(~(good >> (at & 31) & ((1u << kSlotNodes) - 1))) - 1);
+            x.last = x.count < kSlotNodes || at + kSlotNodes >= n;
+            const size_t row = (size_t)b * T;
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) {
+                const int node = half * kHalf + c;
+                const int t = __shfl_sync(0xffffffffu, entry, (at & 31) + node);
+                if (node < x.count) {
+                    const size_t krow = (row + t) * HK + hk, vrow = (row + t) * HV + hv;
+                    x.k[c].load(k + krow * kD + 4 * lane);
+                    x.v[c].load(v + vrow * kD + 4 * lane);
+                    if (!GS) x.g[c] = load4(g + vrow * kD + 4 * lane);
+                    if (lane == node) x.beta = beta[vrow];
+                    if (GS && lane == node) x.gate = g[vrow];
+                }
+            }
+        };
+        // to the next nodes; false behind the last head
+        auto advance = [&](bool last) -> bool {
+            if (!last) {
+                at += kSlotNodes;
+                if ((at & 31) == 0) entry = entries(b, at, n);
+                return true;
+            }
+            head_i += kGroups;
+            if (head_i >= my) return false;
+            b = next_b();
+            hv += step_h;
+            if (hv >= HV) hv -= HV;
+            hk = hv / per_key;
+            at = 0;
+            n = n_next;
+            entry = entry_next;
+            if (head_i + kGroups < my) entry_next = entries(next_b(), 0, n_next);
+            return true;
+        };
+        // puts nodes x, of head this_head, into the group's slot number `number`
+        auto place = [&](const Nodes &x, int this_head, int number) {
+            states(this_head, this_head);  // the group may wait for it before it frees a slot
+            const int to = number % kSlots;
+            Slot &slot = sh.slot[grp][to];
+            if (ok && number >= kSlots)
+                ok = warp_wait(&sh.empty[grp][to], (uint32_t)(number / kSlots - 1) & 1u);
+            if (!ok) return;
+            states(this_head, this_head + kGroups);
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) {
+                const int j = half * kHalf + c;
+                const float gate = GS ? __shfl_sync(0xffffffffu, x.gate, j) : 0.f;
+                if (j < x.count) {
+                    store4(&slot.k[j][4 * lane], x.k[c].f32());
+                    store4(&slot.v[j][4 * lane], x.v[c].f32());
+                    float4 a;
+                    if (GS) {
+                        a.x = a.y = a.z = a.w = expf(gate);
+                    } else {
+                        a = make_float4(expf(x.g[c].x), expf(x.g[c].y), expf(x.g[c].z),
+                                        expf(x.g[c].w));
+                    }
+                    store4(&slot.a[j][4 * lane], a);
+                }
+            }
+            if (lane / kHalf == half && lane < x.count) slot.beta[lane] = x.beta;
+            if (half == 0 && lane == 0) {
+                slot.count = x.count;
+                slot.last = x.last;
+            }
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&sh.full[grp][to]);
+        };
+        // the loads of one slot's nodes are in flight while the one before is placed
+        Nodes x, y;
+        int x_head = head_i, y_head = 0;
+        bool x_more = head_i < my, y_more = false;
+        if (x_more) load(x);
+        for (int c = 0; ok && x_more; c += 2) {
+            y_more = advance(x.last);
+            y_head = head_i;
+            if (y_more) load(y);
+            place(x, x_head, c);
+            if (!ok || !y_more) break;
+            x_more = advance(y.last);
+            x_head = head_i;
+            if (x_more) load(x);
+            place(y, y_head, c + 1);
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(dev_error, 1);
+            // never leave with loads in flight into this CTA: the last
+            // states asked for, one per buffer at most
+            for (int i = next_state - kGroups, j = 0; half == 0 && h0 && i >= 0 && j < kBufs; i -= kGroups, ++j)
+                sm100::mbar_wait_bounded(&sh.state_full[i % kBufs], (uint32_t)(i / kBufs) & 1u,
+                                         kWaitNs);
+        }
+        return;
+    }
+
+    // ---- group grp
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
+    const int grp = warp / kGroupWarps, cq = lane & 7, rg = lane >> 3;
+    const int col = 32 * (warp % kGroupWarps) + 4 * cq;
+    const bool odd = rg & 1, high = rg & 2;
+    const int mine = col + (odd ? 2 : 0) + (high ? 1 : 0);  // the column whose sum ends here
+    int chunk = 0;
+    for (int i = grp; i < my; i += kGroups) {
+        // The head's nodes first: they are there only after its state was
+        // asked for, before which its buffer's barrier would still tell of the
+        // use before.
+        ok = warp_wait(&sh.full[grp][chunk % kSlots], (uint32_t)(chunk / kSlots) & 1u);
+        if (!ok) break;
+        Pair s[8][2][4];  // [m][pair of rows][column]
+        if (h0) {
+            const int buf = i % kBufs;
+            ok = warp_wait(&sh.state_full[buf], (uint32_t)(i / kBufs) & 1u);
+            if (!ok) break;
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float *row = &sh.state[buf][(4 * rg + 16 * m + 2 * r) * kD + col];
+                    const float4 x = load4(row), y = load4(row + kD);
+                    s[m][r][0] = pair(x.x, y.x);
+                    s[m][r][1] = pair(x.y, y.y);
+                    s[m][r][2] = pair(x.z, y.z);
+                    s[m][r][3] = pair(x.w, y.w);
+                }
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&sh.state_empty[buf]);
+        } else {
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[m][r][e] = pair(0.f, 0.f);
+        }
+        int steps = 0;
+        for (bool last = false; !last; ++chunk) {
+            const int at = chunk % kSlots;
+            ok = warp_wait(&sh.full[grp][at], (uint32_t)(chunk / kSlots) & 1u);
+            if (!ok) break;
+            const Slot &slot = sh.slot[grp][at];
+            const int count = slot.count;
+            last = slot.last;
+            steps += count;
+            for (int c = 0; c < count; ++c) {
+                const float *kr = &slot.k[c][4 * rg], *ar = &slot.a[c][4 * rg];
+                Pair acc[4];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
+                    const ulonglong2 aa = *reinterpret_cast<const ulonglong2 *>(ar + 16 * m);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[m][r][e] = mul2(s[m][r][e], Pair{r ? aa.y : aa.x});
+                            acc[e] = m + r == 0 ? mul2(Pair{kk.x}, s[m][r][e])
+                                                : fma2(Pair{r ? kk.y : kk.x}, s[m][r][e], acc[e]);
+                        }
+                }
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 p = split(acc[e]);
+                    x[e] = p.x + p.y;
+                }
+                // over the four row groups, halving the columns each time
+                float p0 = odd ? x[2] : x[0], p1 = odd ? x[3] : x[1];
+                p0 += __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[2], 8);
+                p1 += __shfl_xor_sync(0xffffffffu, odd ? x[1] : x[3], 8);
+                float sum = high ? p1 : p0;
+                sum += __shfl_xor_sync(0xffffffffu, high ? p0 : p1, 16);
+                const float d = slot.beta[c] * (slot.v[c][mine] - sum);
+                Pair dd[4];  // column e is in row group 2 (e & 1) + (e >> 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y = __shfl_sync(0xffffffffu, d, cq + 8 * (2 * (e & 1) + (e >> 1)));
+                    dd[e] = pair(y, y);
+                }
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[m][r][e] = fma2(Pair{r ? kk.y : kk.x}, dd[e], s[m][r][e]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&sh.empty[grp][at]);
+        }
+        if (!ok) break;
+        if (steps == 0 && h0 == ht) continue;
+        float *to = ht + ((size_t)blockIdx.x + (size_t)i * gridDim.x) * kD * kD + 4 * rg * kD + col;
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float2 x = split(s[m][r][0]), y = split(s[m][r][1]), z = split(s[m][r][2]),
+                             w = split(s[m][r][3]);
+                stg_stream4(to + (16 * m + 2 * r) * kD, make_float4(x.x, y.x, z.x, w.x));
+                stg_stream4(to + (16 * m + 2 * r + 1) * kD, make_float4(x.y, y.y, z.y, w.y));
+            }
+    }
+    if (!ok && lane == 0) atomicOr(dev_error, 1);
+}
+
 struct CommitArgs {
     const void *k, *v;
     const float *g, *beta, *h0;
@@ -180,6 +570,25 @@ cudaError_t launch_bv(const CommitArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <typename Tin, bool GS>
+cudaError_t launch_bulk(const CommitArgs &a, int sms, cudaStream_t stream) {
+    int *err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    const int nheads = a.B * a.HV;  // at most 2^30
+    const int grid = nheads < sms ? nheads : sms;
+    const auto kernel = gdr_commit_bulk_kernel<Tin, GS>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(BulkShared));
+    if (e != cudaSuccess) return e;
+    trace_begin(kKernCommit, stream);
+    kernel<<<grid, kBulkThreads, sizeof(BulkShared), stream>>>(
+        static_cast<const Tin *>(a.k), static_cast<const Tin *>(a.v), a.g, a.beta, a.h0, a.ht,
+        a.path, a.n_path, a.T, a.HK, a.HV, a.max_path, nheads, err);
+    trace_end(kKernCommit, stream);
+    return cudaGetLastError();
+}
+
 // 64 columns per CTA, so that k and exp(g) are staged twice a head; 32 where
 // dv is 32 or where 64 would give fewer CTAs than the device has SMs.
 template <typename Tin, int DK, bool GS>
@@ -188,6 +597,7 @@ cudaError_t launch(const CommitArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    if (DK == kD && a.dv == kD && a.B * a.HV > sms) return launch_bulk<Tin, GS>(a, sms, stream);
     if (a.dv < 64 || (long long)a.B * a.HV * (a.dv / 64) < sms)
         return launch_bv<Tin, DK, 32, GS>(a, stream);
     return launch_bv<Tin, DK, 64, GS>(a, stream);

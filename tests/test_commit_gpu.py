@@ -75,6 +75,18 @@ def test_numbers_of_heads(B, HK, HV):
     check(d, *paths(B, 6, 6, seed=B))
 
 
+@pytest.mark.parametrize("h0", [True, False])
+@pytest.mark.parametrize("scalar", [False, True])
+def test_many_heads_of_all_lengths(scalar, h0):
+    """More heads than the device holds at once, several times over; lengths that differ from
+    head to head, so that no two of them take the same time."""
+    d = draw(60, 40, 8, 32, 128, 128, dtype=torch.bfloat16, h0=h0, seed=20, scalar_gate=scalar)
+    p = paths(60, 40, 40, lengths=[1, 4, 0, 9, 2, 37, 5, 1, 8, 3, 40, 1, 1, 12])
+    ht = check(d, *p)
+    for _ in range(3):
+        assert torch.equal(ht, check(d, *p, in_place=h0))
+
+
 def test_long_path_of_512():
     d = draw(1, 512, 1, 2, 128, 128, dtype=torch.float32, seed=4)
     check(d, *paths(1, 512, 512, lengths=[512]))
