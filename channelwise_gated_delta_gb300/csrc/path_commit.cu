@@ -60,7 +60,7 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
 
 // One CTA: BV columns of one head (BV / 16 warps).
 template <typename Tin, int DK, int BV, bool GS>
-__global__ void __launch_bounds__(2 * BV, BV == 64 ? 4 : 8)
+__global__ void __launch_bounds__(2 * BV, (DK == 128 ? 3 : 4) * 64 / BV)
     gdr_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v,
                       const float *__restrict__ g, const float *__restrict__ beta,
                       const float *h0, float *ht, const int *__restrict__ path,
@@ -86,35 +86,57 @@ __global__ void __launch_bounds__(2 * BV, BV == 64 ? 4 : 8)
         s[m][0] = pair(x.x, x.y);
         s[m][1] = pair(x.z, x.w);
     }
-    for (int at = 0; at < n; at += kNodes) {
-        // the nodes of this batch, one per lane; the path ends before the first invalid one
-        int node = -1;
-        if (lane < kNodes && at + lane < n) node = path[(size_t)b * max_path + at + lane];
-        const unsigned bad = __ballot_sync(0xffffffffu, node < 0 || node >= T);
-        const int cnt = min(kNodes, __ffs(bad) - 1);  // lanes past kNodes are bad
-        if (at > 0) __syncthreads();  // the batch before has been used
-#pragma unroll 4
-        for (int i = 0; i < kNodes * DK / NT; ++i) {
-            const int idx = i * NT + tid, c = idx / DK, r = idx % DK;
-            const int t = __shfl_sync(0xffffffffu, node, c);
+    // The nodes of a batch are loaded while the batch before is worked through.
+    // Element i of a thread's loads is that of node (i NT + tid) / DK (of k
+    // and g; v: / BV); `entry` holds the path's entries at & ~31 + lane.
+    constexpr int kK = kNodes * DK / NT, kV = kNodes * BV / NT;
+    Tin kx[kK], vx[kV];
+    float gx[kK], bt = 0.f;
+    int entry = -1, cnt = 0;
+    auto load = [&](int at) {
+        if ((at & 31) == 0)
+            entry = at + lane < n ? path[(size_t)b * max_path + at + lane] : -1;
+        // the path ends before the first invalid entry
+        const unsigned good = __ballot_sync(0xffffffffu, entry >= 0 && entry < T);
+        cnt = min(kNodes, __ffs(~(good >> (at & 31) & ((1u << kNodes) - 1))) - 1);
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            const int c = (i * NT + tid) / DK, r = (i * NT + tid) % DK;
+            const int t = __shfl_sync(0xffffffffu, entry, (at & 31) + c);
             if (c < cnt) {
                 const size_t row = (size_t)b * T + t;
-                const float kk = to_f32(k[(row * HK + hk) * DK + r]);
-                const float a = expf(GS ? g[row * HV + hv] : g[(row * HV + hv) * DK + r]);
-                s_ka[c][r] = make_float4(kk, kk, a, a);
+                kx[i] = k[(row * HK + hk) * DK + r];
+                gx[i] = GS ? g[row * HV + hv] : g[(row * HV + hv) * DK + r];
             }
         }
 #pragma unroll
-        for (int i = 0; i < kNodes * BV / NT; ++i) {
-            const int idx = i * NT + tid, c = idx / BV, j = idx % BV;
-            const int t = __shfl_sync(0xffffffffu, node, c);
-            if (c < cnt)
-                s_v[c][j] = to_f32(v[(((size_t)b * T + t) * HV + hv) * dv + tile * BV + j]);
+        for (int i = 0; i < kV; ++i) {
+            const int c = (i * NT + tid) / BV, j = (i * NT + tid) % BV;
+            const int t = __shfl_sync(0xffffffffu, entry, (at & 31) + c);
+            if (c < cnt) vx[i] = v[(((size_t)b * T + t) * HV + hv) * dv + tile * BV + j];
         }
-        float bt = 0.f;
-        if (lane < cnt) bt = beta[((size_t)b * T + node) * HV + hv];
+        const int t = __shfl_sync(0xffffffffu, entry, (at & 31) + lane % kNodes);
+        if (lane < cnt) bt = beta[((size_t)b * T + t) * HV + hv];
+    };
+    if (n > 0) load(0);
+    for (int at = 0; at < n; at += kNodes) {
+        if (at > 0) __syncthreads();  // the batch before has been used
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            const int c = (i * NT + tid) / DK, r = (i * NT + tid) % DK;
+            const float kk = to_f32(kx[i]), a = expf(gx[i]);
+            if (c < cnt) s_ka[c][r] = make_float4(kk, kk, a, a);
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int c = (i * NT + tid) / BV, j = (i * NT + tid) % BV;
+            if (c < cnt) s_v[c][j] = to_f32(vx[i]);
+        }
+        const float b_batch = bt;
+        const int steps = cnt;
         __syncthreads();
-        for (int c = 0; c < cnt; ++c) {
+        if (steps == kNodes && at + kNodes < n) load(at + kNodes);
+        for (int c = 0; c < steps; ++c) {
             // decay, and the columns' sums over this lane's rows
             Pair acc[2][2];
 #pragma unroll
@@ -139,7 +161,7 @@ __global__ void __launch_bounds__(2 * BV, BV == 64 ? 4 : 8)
             sum += __shfl_xor_sync(0xffffffffu, high ? p0 : p1, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int mine = 4 * cq + (odd ? 2 : 0) + (high ? 1 : 0);
-            const float b_t = __shfl_sync(0xffffffffu, bt, c);
+            const float b_t = __shfl_sync(0xffffffffu, b_batch, c);
             const float d = b_t * (s_v[c][warp * kWarpCols + mine] - sum);
             const Pair d0 = pair(__shfl_sync(0xffffffffu, d, cq), __shfl_sync(0xffffffffu, d, cq + 8));
             const Pair d1 =
@@ -151,7 +173,7 @@ __global__ void __launch_bounds__(2 * BV, BV == 64 ? 4 : 8)
                 s[m][1] = fma2(kk, d1, s[m][1]);
             }
         }
-        if (cnt < kNodes) break;
+        if (steps < kNodes) break;
     }
     float *to = ht + base;
 #pragma unroll
@@ -161,7 +183,7 @@ __global__ void __launch_bounds__(2 * BV, BV == 64 ? 4 : 8)
     }
 }
 
-// ---- dk = dv = 128 and many heads: persistent, the 64 KB states by bulk copies.
+// ---- dk = dv = 128: persistent, the 64 KB states by bulk copies.
 //
 // One CTA per SM walks heads blockIdx.x, + gridDim.x, ...  The kernel above
 // waits for a chain of loads (path length, path, k / g / v of its nodes)
@@ -238,10 +260,13 @@ __device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// A wait of a whole warp, with the same answer in every lane.  The waits here
-// are short and many, so the warp polls rather than sleeps; it looks at
-// the clock every 1024 polls.
+// A wait of a whole warp, with the same answer in every lane.  A group polls,
+// looking at the clock every 1024 polls; a producer sleeps in the barrier, so
+// as not to take issue slots from the groups it waits for.
+template <bool SLEEP>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    if (SLEEP)
+        return __all_sync(0xffffffffu, sm100::mbar_wait_bounded(bar, parity, kWaitNs));
     if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = sm100::global_timer_ns();
     for (int n = 0;; ++n) {
@@ -300,7 +325,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
                 if (use > 0) {
                     const uint32_t parity = (uint32_t)(use - 1) & 1u;
                     if (next_state <= upto)
-                        ok = warp_wait(&sh.state_empty[buf], parity);
+                        ok = warp_wait<true>(&sh.state_empty[buf], parity);
                     else if (!__all_sync(0xffffffffu, test_wait(&sh.state_empty[buf], parity)))
                         break;
                 }
@@ -383,7 +408,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
             const int to = number % kSlots;
             Slot &slot = sh.slot[grp][to];
             if (ok && number >= kSlots)
-                ok = warp_wait(&sh.empty[grp][to], (uint32_t)(number / kSlots - 1) & 1u);
+                ok = warp_wait<true>(&sh.empty[grp][to], (uint32_t)(number / kSlots - 1) & 1u);
             if (!ok) return;
             states(this_head, this_head + kGroups);
 #pragma unroll
@@ -449,12 +474,12 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
         // The head's nodes first: they are there only after its state was
         // asked for, before which its buffer's barrier would still tell of the
         // use before.
-        ok = warp_wait(&sh.full[grp][chunk % kSlots], (uint32_t)(chunk / kSlots) & 1u);
+        ok = warp_wait<false>(&sh.full[grp][chunk % kSlots], (uint32_t)(chunk / kSlots) & 1u);
         if (!ok) break;
         Pair s[8][2][4];  // [m][pair of rows][column]
         if (h0) {
             const int buf = i % kBufs;
-            ok = warp_wait(&sh.state_full[buf], (uint32_t)(i / kBufs) & 1u);
+            ok = warp_wait<false>(&sh.state_full[buf], (uint32_t)(i / kBufs) & 1u);
             if (!ok) break;
 #pragma unroll
             for (int m = 0; m < 8; ++m)
@@ -480,7 +505,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
         int steps = 0;
         for (bool last = false; !last; ++chunk) {
             const int at = chunk % kSlots;
-            ok = warp_wait(&sh.full[grp][at], (uint32_t)(chunk / kSlots) & 1u);
+            ok = warp_wait<false>(&sh.full[grp][at], (uint32_t)(chunk / kSlots) & 1u);
             if (!ok) break;
             const Slot &slot = sh.slot[grp][at];
             const int count = slot.count;
@@ -597,7 +622,7 @@ cudaError_t launch(const CommitArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (DK == kD && a.dv == kD && a.B * a.HV > sms) return launch_bulk<Tin, GS>(a, sms, stream);
+    if (DK == kD && a.dv == kD) return launch_bulk<Tin, GS>(a, sms, stream);
     if (a.dv < 64 || (long long)a.B * a.HV * (a.dv / 64) < sms)
         return launch_bv<Tin, DK, 32, GS>(a, stream);
     return launch_bv<Tin, DK, 64, GS>(a, stream);
