@@ -32,31 +32,65 @@ constexpr int kMaxVocab = 1 << 22;  // 2^22 weights of at most 2^40 each: sums b
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;  // the portable limit
-constexpr int kAhead = 4;       // 16-byte loads a lane has in flight per row
+constexpr int kAheadF32 = 4;    // 16-byte loads a lane has in flight per row (bf16: half)
 constexpr float kUnit = 1099511627776.f;            // 2^40
 constexpr float kUnitInv = 9.094947017729282e-13f;  // 2^-40
 constexpr int kUBits = 24;
 
 // A probability as it counts: NaN and negative 0, above 1 at most 1.
-__device__ __forceinline__ float probability(float x) {
-    return fminf(fmaxf(x, 0.f), 1.f);  // fmaxf(NaN, 0) = 0
+__device__ __forceinline__ float probability(float x) { return __saturatef(x); }
+
+// Sums of fix(x) = floor(2^40 x) for 0 <= x < 4.  A conversion to 64-bit whole
+// numbers runs at the FP64 pipe's rate (it took two thirds of the call), so x
+// is taken apart by float operations, all of them exact: added to 2^23 and
+// rounded towards zero, a number below 2^23 leaves its whole part in the
+// low bits of the sum.  floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x)
+// and lo the same of what is left of it.
+struct Mass {
+    uint32_t hi = 0, lo = 0;  // of at most 1024 elements
+    long long sum = 0;
+    __device__ __forceinline__ void add(float x) {
+        constexpr float kTwo20 = 1048576.f, kTwo23 = 8388608.f;
+        const float y = __fmul_rn(x, kTwo20);
+        const float whole = __fadd_rz(y, kTwo23);
+        const float rest = __fsub_rn(y, __fsub_rn(whole, kTwo23));
+        hi += __float_as_uint(whole) - 0x4b000000u;
+        lo += __float_as_uint(__fmaf_rz(rest, kTwo20, kTwo23)) - 0x4b000000u;
+    }
+    __device__ __forceinline__ void flush() {
+        sum += ((long long)hi << 20) + lo;
+        hi = lo = 0;
+    }
+};
+__device__ __forceinline__ long long fix(float x) {
+    Mass m;
+    m.add(x);
+    m.flush();
+    return m.sum;
 }
-__device__ __forceinline__ long long fix(float x) { return __float2ll_rz(__fmul_rn(x, kUnit)); }
 __device__ __forceinline__ float mass_of(long long sum) {
     return __fmul_rn(__ll2float_rn(sum), kUnitInv);
 }
 
-// An element's weight after n refusals with q: the residual of the last one
-// that left something (P before any); norm[s] is the mass of residual s, 0
-// where it had none.
-__device__ __forceinline__ float residual(float P, float Q, const float *norm, int n) {
-    float weight = P, scaled = P;
+// The weights of M elements after n refusals with q, given P in w and Q in x:
+// the residual of the last refusal that left something (P before any);
+// norm[s] is the mass of residual s, 0 where it had none.  All elements take
+// a refusal together, for the latency of the division.
+template <int M>
+__device__ __forceinline__ void residuals(float (&w)[M], const float (&x)[M], const float *norm,
+                                          int n) {
+    float scale = 1.f;  // of the refusal before
     for (int s = 0; s < n; ++s) {
-        if (norm[s] == 0.f) continue;
-        weight = fmaxf(__fsub_rn(scaled, Q), 0.f);
-        if (s + 1 < n) scaled = __fdiv_rn(weight, norm[s]);
+        const float mass = norm[s];
+        if (mass == 0.f) continue;
+        if (scale != 1.f) {
+#pragma unroll
+            for (int e = 0; e < M; ++e) w[e] = __fdiv_rn(w[e], scale);
+        }
+#pragma unroll
+        for (int e = 0; e < M; ++e) w[e] = fmaxf(__fsub_rn(w[e], x[e]), 0.f);
+        scale = mass;
     }
-    return weight;
 }
 
 // ---- a row of V elements, addressed by j = i + shift, shift being the
@@ -137,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                       long long parent_sb, long long parent_st, int max_path, int cluster) {
     constexpr int N = Vec<Tp>::N;
     constexpr int kWide = 32 * N;  // elements of a warp's load: a unit of the row
+    constexpr int kAhead = kAheadF32 * 4 / N;
     __shared__ int s_parent[kMaxNodes], s_token[kMaxNodes];
     __shared__ float s_coin[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
     __shared__ float s_norm[kMaxNodes];   // with q: the mass of each residual
@@ -189,41 +224,49 @@ __global__ void __launch_bounds__(kThreads, 4)
         u0 = min(c0 + warp * per_warp, c1);
         u1 = min(u0 + per_warp, c1);
     };
-    // weights of the elements of a lane's vector; refusals without q are taken off elsewhere
-    auto weights = [&](uint4 pv, uint4 qv, int n, float (&w)[N]) {
-        unpack(pv, w);
+    // the weights of K vectors of a lane; refusals without q are taken off elsewhere
+    auto weights = [&](const auto &pv, const auto &qv, int n, auto &w) {
+        constexpr int K = sizeof(pv) / sizeof(uint4);
 #pragma unroll
-        for (int e = 0; e < N; ++e) w[e] = probability(w[e]);
+        for (int k = 0; k < K; ++k) {
+            float y[N];
+            unpack(pv[k], y);
+#pragma unroll
+            for (int e = 0; e < N; ++e) w[k * N + e] = probability(y[e]);
+        }
         if (HAS_Q && n > 0) {
-            float x[N];
-            unpack(qv, x);
+            float x[K * N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = probability(x[e]);
+            for (int k = 0; k < K; ++k) {
+                float y[N];
+                unpack(qv[k], y);
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[k * N + e] = probability(y[e]);
+            }
             if (n == 1 && s_norm[0] != 0.f) {  // nearly every row that is read whole
 #pragma unroll
-                for (int e = 0; e < N; ++e) w[e] = fmaxf(__fsub_rn(w[e], x[e]), 0.f);
+                for (int e = 0; e < K * N; ++e) w[e] = __saturatef(__fsub_rn(w[e], x[e]));
             } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) w[e] = residual(w[e], x[e], s_norm, n);
+                residuals(w, x, s_norm, n);
             }
         }
     };
     // the weights of this lane's elements of a unit
     auto unit_weights = [&](int unit, int n, float (&w)[N]) {
         const int i0 = unit * kWide + lane * N - shift;
-        uint4 pv, qv = make_uint4(0u, 0u, 0u, 0u);
+        uint4 pv[1], qv[1] = {make_uint4(0u, 0u, 0u, 0u)};
         if (unit >= f0 && unit < f1) {
-            pv = load_vec(prow, i0);
-            if (HAS_Q && n > 0) qv = load_vec(qrow, i0);
+            pv[0] = load_vec(prow, i0);
+            if (HAS_Q && n > 0) qv[0] = load_vec(qrow, i0);
         } else {
-            pv = load_elements(prow, i0, V);
-            if (HAS_Q && n > 0) qv = load_elements(qrow, i0, V);
+            pv[0] = load_elements(prow, i0, V);
+            if (HAS_Q && n > 0) qv[0] = load_elements(qrow, i0, V);
         }
         weights(pv, qv, n, w);
     };
     // mass of units lo .. hi - 1 after n refusals, in every lane of the warp
     auto mass = [&](int lo, int hi, int n) -> long long {
-        long long part = 0;
+        Mass part;
         for (int at = lo; at < hi; at += kAhead) {
             uint4 pv[kAhead], qv[kAhead];
 #pragma unroll
@@ -233,29 +276,27 @@ __global__ void __launch_bounds__(kThreads, 4)
                 pv[k] = whole ? load_vec(prow, i0) : make_uint4(0u, 0u, 0u, 0u);
                 qv[k] = HAS_Q && n > 0 && whole ? load_vec(qrow, i0) : make_uint4(0u, 0u, 0u, 0u);
             }
-            if (at < f0 || min(at + kAhead, hi) > f1) {
+            if (at < f0 || min(at + kAhead, hi) > f1) {  // the ends of the row, one by one
                 for (int k = 0; k < kAhead; ++k) {
                     if (at + k >= hi || (at + k >= f0 && at + k < f1)) continue;
                     float w[N];
                     unit_weights(at + k, n, w);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) part += fix(w[e]);
+                    for (int e = 0; e < N; ++e) part.add(w[e]);
                 }
             }
+            float w[kAhead * N];
+            weights(pv, qv, n, w);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                float w[N];
-                weights(pv[k], qv[k], n, w);
-#pragma unroll
-                for (int e = 0; e < N; ++e) part += fix(w[e]);
-            }
+            for (int e = 0; e < kAhead * N; ++e) part.add(w[e]);
+            part.flush();
         }
         if (!HAS_Q)
             for (int s = lane; s < n; s += 32) {
                 const int unit = (s_token[s_refused[s]] + shift) / kWide;
-                if (unit >= lo && unit < hi) part -= fix(s_p[s_refused[s]]);
+                if (unit >= lo && unit < hi) part.sum -= fix(s_p[s_refused[s]]);
             }
-        return warp_sum(part);
+        return warp_sum(part.sum);
     };
     int round = 0;
     // total mass of the node's rows after n refusals; each warp's in s_warp,
@@ -418,13 +459,11 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
         if (upto - own <= goal && goal < upto) {
             long long run = upto - own;
-            int found = 0;
+            int found = -1;  // the first element whose running sum is above
 #pragma unroll
-            for (int e = N - 1; e >= 0; --e) {  // the first element whose running sum is above
-                long long sum = run;
-#pragma unroll
-                for (int k = 0; k <= e; ++k) sum += fix(x[k]);
-                if (sum > goal) found = e;
+            for (int e = 0; e < N; ++e) {
+                run += fix(x[e]);
+                if (found < 0 && run > goal) found = e;
             }
             next_token[b] = j0 + found - shift;
         }
