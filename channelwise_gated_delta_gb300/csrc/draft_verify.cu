@@ -29,8 +29,6 @@ namespace {
 
 constexpr int kMaxNodes = 512;
 constexpr int kMaxVocab = 1 << 22;  // 2^22 weights of at most 2^40 each: sums below 2^63
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;  // the portable limit
 constexpr int kAheadF32 = 4;    // 16-byte loads a lane has in flight per row (bf16: half)
 constexpr float kUnit = 1099511627776.f;            // 2^40
@@ -72,6 +70,12 @@ __device__ __forceinline__ float mass_of(long long sum) {
     return __fmul_rn(__ll2float_rn(sum), kUnitInv);
 }
 
+// w / mass for a residual's w >= 0.  Half of a residual is zeros, and a
+// zero would take the division's slow path.
+__device__ __forceinline__ float divided(float w, float mass) {
+    const float x = __fdiv_rn(w > 0.f ? w : mass, mass);
+    return w > 0.f ? x : 0.f;
+}
 // The weights of M elements after n refusals with q, given P in w and Q in x:
 // the residual of the last refusal that left something (P before any);
 // norm[s] is the mass of residual s, 0 where it had none.  All elements take
@@ -85,7 +89,7 @@ __device__ __forceinline__ void residuals(float (&w)[M], const float (&x)[M], co
         if (mass == 0.f) continue;
         if (scale != 1.f) {
 #pragma unroll
-            for (int e = 0; e < M; ++e) w[e] = __fdiv_rn(w[e], scale);
+            for (int e = 0; e < M; ++e) w[e] = divided(w[e], scale);
         }
 #pragma unroll
         for (int e = 0; e < M; ++e) w[e] = fmaxf(__fsub_rn(w[e], x[e]), 0.f);
@@ -161,14 +165,18 @@ __device__ __forceinline__ void store_remote(long long *var, int rank, long long
         : "memory");
 }
 
-template <typename Tp, bool HAS_Q>
-__global__ void __launch_bounds__(kThreads, 4)
+// KEEP: a lane's part of the rows is at most kAhead vectors and stays in
+// registers while the walk is at their node, for further refusals and for the
+// search.  THREADS threads per CTA, 1024 / THREADS CTAs per SM.
+template <typename Tp, bool HAS_Q, bool KEEP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     gdr_verify_kernel(const Tp *__restrict__ p, const Tp *__restrict__ q,
                       const int *__restrict__ tokens, const int *__restrict__ parent,
                       const float *__restrict__ coins, const float *__restrict__ u,
                       int *__restrict__ path, int *__restrict__ n_path,
                       int *__restrict__ next_token, int T, int V, long long ldp, long long ldq,
                       long long parent_sb, long long parent_st, int max_path, int cluster) {
+    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
     constexpr int N = Vec<Tp>::N;
     constexpr int kWide = 32 * N;  // elements of a warp's load: a unit of the row
     constexpr int kAhead = kAheadF32 * 4 / N;
@@ -182,25 +190,6 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / cluster, rank = blockIdx.x - b * cluster;
     cluster_arrive();  // (1) this CTA runs: its shared memory may be written
-
-    for (int t = tid; t < T; t += kThreads) {
-        const size_t at = (size_t)b * T + t;
-        int par = -1, tok = -1;
-        if (t > 0) {
-            par = parent[b * parent_sb + t * parent_st];
-            tok = tokens[at];
-        }
-        const float coin = coins[at];
-        const bool ok = par >= 0 && par < t && tok >= 0 && tok < V;
-        const size_t row = (size_t)b * T + (ok ? par : 0);
-        s_p[t] = ok ? probability(to_f32(p[row * ldp + tok])) : 0.f;
-        s_q[t] = ok && HAS_Q ? probability(to_f32(q[row * ldq + tok])) : 0.f;
-        s_parent[t] = ok ? par : -1;
-        s_token[t] = tok;
-        s_coin[t] = coin;
-    }
-    const float uu = u[b];
-    __syncthreads();
 
     // ---- this warp's part of the rows of the node reached
     const Tp *prow = nullptr, *qrow = nullptr;
@@ -251,23 +240,45 @@ __global__ void __launch_bounds__(kThreads, 4)
             }
         }
     };
+    // a lane's vectors of unit `unit`, zeros behind unit `end`
+    auto load_unit = [&](int unit, int end, bool with_q, uint4 &pv, uint4 &qv) {
+        const int i0 = unit * kWide + lane * N - shift;
+        pv = qv = make_uint4(0u, 0u, 0u, 0u);
+        if (unit >= f0 && unit < min(end, f1)) {
+            pv = load_vec(prow, i0);
+            if (with_q) qv = load_vec(qrow, i0);
+        } else if (unit < end) {  // at the ends of the row one by one
+            pv = load_elements(prow, i0, V);
+            if (with_q) qv = load_elements(qrow, i0, V);
+        }
+    };
     // the weights of this lane's elements of a unit
     auto unit_weights = [&](int unit, int n, float (&w)[N]) {
-        const int i0 = unit * kWide + lane * N - shift;
-        uint4 pv[1], qv[1] = {make_uint4(0u, 0u, 0u, 0u)};
-        if (unit >= f0 && unit < f1) {
-            pv[0] = load_vec(prow, i0);
-            if (HAS_Q && n > 0) qv[0] = load_vec(qrow, i0);
-        } else {
-            pv[0] = load_elements(prow, i0, V);
-            if (HAS_Q && n > 0) qv[0] = load_elements(qrow, i0, V);
-        }
+        uint4 pv[1], qv[1];
+        load_unit(unit, units, HAS_Q && n > 0, pv[0], qv[0]);
         weights(pv, qv, n, w);
+    };
+    // KEEP: the rows of node `held`
+    uint4 kept_p[KEEP ? kAhead : 1], kept_q[KEEP ? kAhead : 1];
+    int held = -1;
+    auto hold = [&](int node) {
+        if (!KEEP || node == held) return;
+        held = node;
+        take_rows(node);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) load_unit(u0 + k, u1, HAS_Q, kept_p[KEEP ? k : 0], kept_q[KEEP ? k : 0]);
     };
     // mass of units lo .. hi - 1 after n refusals, in every lane of the warp
     auto mass = [&](int lo, int hi, int n) -> long long {
         Mass part;
-        for (int at = lo; at < hi; at += kAhead) {
+        if (KEEP) {  // lo .. hi - 1 are this warp's own units
+            float w[(KEEP ? kAhead : 1) * N];
+            weights(kept_p, kept_q, n, w);
+#pragma unroll
+            for (int e = 0; e < (KEEP ? kAhead : 1) * N; ++e) part.add(w[e]);
+            part.flush();
+        }
+        for (int at = lo; !KEEP && at < hi; at += kAhead) {
             uint4 pv[kAhead], qv[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
@@ -298,6 +309,26 @@ __global__ void __launch_bounds__(kThreads, 4)
             }
         return warp_sum(part.sum);
     };
+    if (KEEP) hold(0);  // in flight with the nodes: the walk may well end at the root
+    for (int t = tid; t < T; t += kThreads) {
+        const size_t at = (size_t)b * T + t;
+        int par = -1, tok = -1;
+        if (t > 0) {
+            par = parent[b * parent_sb + t * parent_st];
+            tok = tokens[at];
+        }
+        const float coin = coins[at];
+        const bool ok = par >= 0 && par < t && tok >= 0 && tok < V;
+        const size_t row = (size_t)b * T + (ok ? par : 0);
+        s_p[t] = ok ? probability(to_f32(p[row * ldp + tok])) : 0.f;
+        s_q[t] = ok && HAS_Q ? probability(to_f32(q[row * ldq + tok])) : 0.f;
+        s_parent[t] = ok ? par : -1;
+        s_token[t] = tok;
+        s_coin[t] = coin;
+    }
+    const float uu = u[b];
+    __syncthreads();
+
     int round = 0;
     // total mass of the node's rows after n refusals; each warp's in s_warp,
     // each CTA's in s_total[round & 1]
@@ -351,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                     a = s_p[t];
                     for (int s = 0; s < out; ++s)
                         if (s_norm[s] != 0.f)
-                            a = __fdiv_rn(fmaxf(__fsub_rn(a, s_q[t]), 0.f), s_norm[s]);
+                            a = divided(fmaxf(__fsub_rn(a, s_q[t]), 0.f), s_norm[s]);
                     bar = __fmul_rn(s_coin[t], s_q[t]);
                 } else {
                     bool again = false;
@@ -392,7 +423,10 @@ __global__ void __launch_bounds__(kThreads, 4)
         out = s_out;
         summed = s_summed;
         if (!HAS_Q || !s_more) break;
-        take_rows(here);
+        if (KEEP)
+            hold(here);
+        else
+            take_rows(here);
         total = total_mass(out);
         summed = total > 0;  // without mass the weights stay those of before
         if (tid == 0) s_norm[out - 1] = mass_of(total);
@@ -405,7 +439,10 @@ __global__ void __launch_bounds__(kThreads, 4)
 
     // ---- the next token
     if (!HAS_Q || !summed) {
-        take_rows(here);
+        if (KEEP)
+            hold(here);
+        else
+            take_rows(here);
         total = total_mass(out);
     }
     if (!HAS_Q && total == 0 && out > 0) {  // nothing left: the row as it was
@@ -423,9 +460,55 @@ __global__ void __launch_bounds__(kThreads, 4)
     const long long *totals = s_total[round & 1];
     for (int r = 0; r < rank; ++r) goal -= totals[r];
     if (goal < 0 || goal >= totals[rank]) return;
-    // the warp, then an eighth of its units, then the element
     int w = 0;
     for (; goal >= s_warp[w]; ++w) goal -= s_warp[w];
+    // looks for the goal among a unit's elements, of weights x; takes the unit's mass off it
+    auto in_unit = [&](int unit, float (&x)[N]) -> bool {
+        const int i0 = unit * kWide + lane * N - shift;
+        if (!HAS_Q)
+            for (int s = 0; s < out; ++s) {
+                const int e = s_token[s_refused[s]] - i0;
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (k == e) x[k] = 0.f;
+            }
+        Mass own;
+#pragma unroll
+        for (int e = 0; e < N; ++e) own.add(x[e]);
+        own.flush();
+        long long upto = own.sum;  // of the lanes up to this one
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        if (upto - own.sum <= goal && goal < upto) {
+            long long run = upto - own.sum;
+            int found = -1;  // the first element whose running sum is above
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                run += fix(x[e]);
+                if (found < 0 && run > goal) found = e;
+            }
+            next_token[b] = i0 + found;
+        }
+        const long long all = __shfl_sync(0xffffffffu, upto, 31);
+        const bool hit = goal < all;
+        goal -= all;
+        return hit;
+    };
+    if (KEEP) {
+        if (w != warp) return;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint4 pv[1] = {kept_p[KEEP ? k : 0]}, qv[1] = {kept_q[KEEP ? k : 0]};
+            float x[N];
+            weights(pv, qv, out, x);
+            if (in_unit(u0 + k, x)) return;
+        }
+        return;
+    }
+    // the warp's units divided among all warps of the CTA, then one by one
     const int per_cta = (units + cluster - 1) / cluster, c1 = min(c0 + per_cta, units);
     const int w0 = min(c0 + w * per_warp, c1), w1 = min(w0 + per_warp, c1);
     const int step = (w1 - w0 + kWarps - 1) / kWarps;
@@ -438,88 +521,73 @@ __global__ void __launch_bounds__(kThreads, 4)
     for (; goal >= s_warp[w]; ++w) goal -= s_warp[w];
     if (w != warp) return;
     for (int at = m0; at < m1; ++at) {
-        const int j0 = at * kWide + lane * N;
         float x[N];
         unit_weights(at, out, x);
-        if (!HAS_Q)
-            for (int s = 0; s < out; ++s) {
-                const int e = s_token[s_refused[s]] + shift - j0;
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (k == e) x[k] = 0.f;
-            }
-        long long own = 0;
-#pragma unroll
-        for (int e = 0; e < N; ++e) own += fix(x[e]);
-        long long upto = own;  // of the lanes up to this one
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
-        }
-        if (upto - own <= goal && goal < upto) {
-            long long run = upto - own;
-            int found = -1;  // the first element whose running sum is above
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                run += fix(x[e]);
-                if (found < 0 && run > goal) found = e;
-            }
-            next_token[b] = j0 + found - shift;
-        }
-        const long long all = __shfl_sync(0xffffffffu, upto, 31);
-        if (goal < all) return;
-        goal -= all;
+        if (in_unit(at, x)) return;
     }
 }
 
-// CTAs per tree: a power of two up to the cluster limit, doubled while all
-// the trees' CTAs would leave the device's slots (4 a SM) empty and each would keep at
-// least 1024 elements.
-int cluster_size(int B, int V, int sms) {
-    int c = 1;
-    while (c < kMaxCluster && (long long)B * c < 4LL * sms && V / (2 * c) >= 1024) c *= 2;
-    return c;
-}
+struct VerifyArgs {
+    const void *p, *q;
+    const int *tokens, *parent;
+    const float *coins, *u;
+    int *path, *n_path, *next_token;
+    int B, T, V;
+    long long ldp, ldq, parent_sb, parent_st;
+    int max_path;
+};
 
-template <typename Tp, bool HAS_Q>
-cudaError_t launch_q(const void *p, const void *q, const int *tokens, const int *parent,
-                     const float *coins, const float *u, int *path, int *n_path, int *next_token,
-                     int B, int T, int V, long long ldp, long long ldq, long long parent_sb,
-                     long long parent_st, int max_path, cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const int c = cluster_size(B, V, sms);
-    if ((long long)B * c > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+template <typename Tp, bool HAS_Q, bool KEEP, int THREADS>
+cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
+    if ((long long)a.B * c > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = c;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(B * c));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)(a.B * c));
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     trace_begin(kKernVerify, stream);
-    e = cudaLaunchKernelEx(&cfg, gdr_verify_kernel<Tp, HAS_Q>, static_cast<const Tp *>(p),
-                           static_cast<const Tp *>(q), tokens, parent, coins, u, path, n_path,
-                           next_token, T, V, ldp, ldq, parent_sb, parent_st, max_path, c);
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, gdr_verify_kernel<Tp, HAS_Q, KEEP, THREADS>, static_cast<const Tp *>(a.p),
+        static_cast<const Tp *>(a.q), a.tokens, a.parent, a.coins, a.u, a.path, a.n_path,
+        a.next_token, a.T, a.V, a.ldp, a.ldq, a.parent_sb, a.parent_st, a.max_path, c);
     trace_end(kKernVerify, stream);
     return e;
 }
 
-template <typename Tp>
-cudaError_t launch(const void *p, const void *q, const int *tokens, const int *parent,
-                   const float *coins, const float *u, int *path, int *n_path, int *next_token,
-                   int B, int T, int V, long long ldp, long long ldq, long long parent_sb,
-                   long long parent_st, int max_path, cudaStream_t stream) {
-    return q ? launch_q<Tp, true>(p, q, tokens, parent, coins, u, path, n_path, next_token, B, T,
-                                  V, ldp, ldq, parent_sb, parent_st, max_path, stream)
-             : launch_q<Tp, false>(p, q, tokens, parent, coins, u, path, n_path, next_token, B, T,
-                                   V, ldp, ldq, parent_sb, parent_st, max_path, stream);
+// CTAs per tree, a power of two up to the cluster limit.  Few trees: as many
+// as SMs and row allow (a CTA has a vector at least for each of 256 threads),
+// with the fewest threads whose lanes can keep their part of the row.  Clusters
+// of 8 do not fill the device (a cluster keeps to one processing cluster of
+// SMs), so 7 of 8 SMs are counted.  Otherwise CTAs of 256 threads that stream
+// the rows, doubled while the trees' CTAs would leave the device's slots (4
+// a SM) empty and each would keep 1024 elements.
+template <typename Tp, bool HAS_Q>
+cudaError_t launch_q(const VerifyArgs &a, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    constexpr int N = Vec<Tp>::N, kKeep = kAheadF32 * 4 / N;
+    int c = 1;
+    while (c < kMaxCluster && (long long)a.B * 2 * c <= sms * 7 / 8 && a.V >= 2 * c * 256 * N)
+        c *= 2;
+    if (a.B <= sms) {
+        // the units of a warp, of a row that may begin anywhere in a vector
+        const int units = (a.V + N - 1 + 32 * N - 1) / (32 * N), per_cta = (units + c - 1) / c;
+        if ((per_cta + 7) / 8 <= kKeep) return launch_clusters<Tp, HAS_Q, true, 256>(a, c, stream);
+        if ((per_cta + 15) / 16 <= kKeep)
+            return launch_clusters<Tp, HAS_Q, true, 512>(a, c, stream);
+        if ((per_cta + 31) / 32 <= kKeep)
+            return launch_clusters<Tp, HAS_Q, true, 1024>(a, c, stream);
+    }
+    c = 1;
+    while (c < kMaxCluster && (long long)a.B * c < 4LL * sms && a.V / (2 * c) >= 1024) c *= 2;
+    return launch_clusters<Tp, HAS_Q, false, 256>(a, c, stream);
 }
 
 // Whether `rows` rows `ld` apart are addressable (element offsets below 2^58).
@@ -565,12 +633,12 @@ extern "C" GDR_API gdr_status gdr_verify_drafts(const void *p, const void *q, co
     for (int o = 6; o < 9; ++o)  // an output against the inputs and the outputs before it
         if (overlaps_any(args[o], args, o)) return GDR_ERR_ALIAS;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const VerifyArgs a{p,   q,   tokens,    parent,    coins,   u, path, n_path, next_token, B, T, V,
+                       ldp, ldq, parent_sb, parent_st, max_path};
     const cudaError_t e =
         prob_dtype == GDR_BF16
-            ? launch<__nv_bfloat16>(p, q, tokens, parent, coins, u, path, n_path, next_token, B, T,
-                                    V, ldp, ldq, parent_sb, parent_st, max_path, s)
-            : launch<float>(p, q, tokens, parent, coins, u, path, n_path, next_token, B, T, V, ldp,
-                            ldq, parent_sb, parent_st, max_path, s);
+            ? (q ? launch_q<__nv_bfloat16, true>(a, s) : launch_q<__nv_bfloat16, false>(a, s))
+            : (q ? launch_q<float, true>(a, s) : launch_q<float, false>(a, s));
     if (e == cudaSuccess) return GDR_OK;
     record_cuda_error(e);
     return GDR_ERR_CUDA;
