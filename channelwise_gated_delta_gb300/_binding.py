@@ -352,27 +352,27 @@ def gdr_forward_tree(q, k, v, g, beta, parent, h0=None, out=None, stream=None, w
     return out
 
 
-def _on_device(dev, *named):
-    """Every named tensor that is given is on the CUDA device ``dev`` and contiguous."""
-    if dev.type != "cuda":
-        raise ValueError("%s must be a CUDA tensor" % named[0][0])
-    for name, t in named:
-        if t is None:
-            continue
-        if t.device != dev:
-            raise ValueError("%s must be a CUDA tensor on %s" % (name, dev))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-
-
-def _is(name, t, shape, dtype):
-    if t.shape != shape or t.dtype != dtype:
+def _given(name, t, shape, dtype, index):
+    """``t`` is a contiguous ``dtype`` tensor of this shape on CUDA device ``index``."""
+    if t.get_device() != index or index < 0:
+        raise ValueError("%s must be a CUDA tensor%s"
+                         % (name, " on cuda:%d" % index if index >= 0 else ""))
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError("%s must be %s %s, got %s %s"
                          % (name, dtype, list(shape), t.dtype, list(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _stream_of(stream, index):
+    """The CUDA stream's address; the current one of device ``index`` for None."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _prob_rows(name, t):
     """The distance of the rows of [B, T, V] probabilities, whose rows may be apart."""
+    if t.is_contiguous():
+        return t.shape[2]
     B, T, V = t.shape
     ld = t.stride(1) if T > 1 else t.stride(0) if B > 1 else V
     if (V > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != T * ld) or ld < V:
@@ -396,43 +396,40 @@ def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=N
     if p.dim() != 3:
         raise ValueError("p must be [B, T, V]")
     B, T, V = p.shape
-    dev = p.device
+    index = p.get_device()
     code = _dtype_code(p.dtype, "p and q")
+    i32 = torch.int32
+    _given("tokens", tokens, (B, T), i32, index)
+    _given("coins", coins, (B, T), torch.float32, index)
+    _given("u", u, (B,), torch.float32, index)
+    if parent.shape != (B, T) or parent.dtype is not i32 or parent.get_device() != index:
+        raise ValueError("parent must be torch.int32 [%d, %d] on cuda:%d" % (B, T, index))
+    ldq, q_ptr = 0, None
+    if q is not None:
+        if q.shape != p.shape or q.dtype is not p.dtype or q.get_device() != index:
+            raise ValueError("q must match p in shape, dtype and device")
+        ldq, q_ptr = _prob_rows("q", q), q.data_ptr()
     if max_path is None:
         max_path = T if path is None else path.shape[-1]
-    _on_device(dev, ("tokens", tokens), ("coins", coins), ("u", u), ("path", path),
-               ("n_path", n_path), ("next_token", next_token))
-    for name, t in (("parent", parent), ("q", q)):  # of any strides: checked below
-        if t is not None and t.device != dev:
-            raise ValueError("%s must be a CUDA tensor on %s" % (name, dev))
-    if q is not None:
-        _is("q", q, p.shape, p.dtype)
-    _is("tokens", tokens, (B, T), torch.int32)
-    _is("parent", parent, (B, T), torch.int32)
-    _is("coins", coins, (B, T), torch.float32)
-    _is("u", u, (B,), torch.float32)
     if path is None:
-        path = torch.empty(B, max_path, dtype=torch.int32, device=dev)
+        path = torch.empty((B, max_path), dtype=i32, device=p.device)
     else:
-        _is("path", path, (B, max_path), torch.int32)
+        _given("path", path, (B, max_path), i32, index)
     if n_path is None:
-        n_path = torch.empty(B, dtype=torch.int32, device=dev)
+        n_path = torch.empty(B, dtype=i32, device=p.device)
     else:
-        _is("n_path", n_path, (B,), torch.int32)
+        _given("n_path", n_path, (B,), i32, index)
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+        next_token = torch.empty(B, dtype=i32, device=p.device)
     else:
-        _is("next_token", next_token, (B,), torch.int32)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    st = lib.gdr_verify_drafts(p.data_ptr(), None if q is None else q.data_ptr(),
-                               tokens.data_ptr(), parent.data_ptr(), coins.data_ptr(),
-                               u.data_ptr(), path.data_ptr(), n_path.data_ptr(),
-                               next_token.data_ptr(), B, T, V, _prob_rows("p", p),
-                               0 if q is None else _prob_rows("q", q), parent.stride(0),
-                               parent.stride(1), max_path,
-                               stream.cuda_stream, code)
-    _check(lib, st)
+        _given("next_token", next_token, (B,), i32, index)
+    st = lib.gdr_verify_drafts(p.data_ptr(), q_ptr, tokens.data_ptr(), parent.data_ptr(),
+                               coins.data_ptr(), u.data_ptr(), path.data_ptr(),
+                               n_path.data_ptr(), next_token.data_ptr(), B, T, V,
+                               _prob_rows("p", p), ldq, parent.stride(0), parent.stride(1),
+                               max_path, _stream_of(stream, index), code)
+    if st != GDR_OK:
+        _check(lib, st)
     return path, n_path, next_token
 
 
@@ -445,35 +442,35 @@ def gdr_commit_path(k, v, g, beta, path, n_path, h0=None, ht=None, stream=None, 
     lib = load_library()
     B, T, HK, dk = k.shape
     HV, dv = v.shape[2], v.shape[3]
-    dev = k.device
+    index = k.get_device()
     code = _dtype_code(k.dtype, "k and v")
-    _on_device(dev, ("k", k), ("v", v), ("g", g), ("beta", beta), ("path", path),
-               ("n_path", n_path), ("h0", h0), ("ht", ht))
-    _is("v", v, (B, T, HV, dv), k.dtype)
-    _is("beta", beta, (B, T, HV), torch.float32)
+    f32 = torch.float32
+    _given("k", k, (B, T, HK, dk), k.dtype, index)
+    _given("v", v, (B, T, HV, dv), k.dtype, index)
+    _given("beta", beta, (B, T, HV), f32, index)
     if g.dim() == 3:  # a scalar gate
         flags |= GDR_FLAG_SCALAR_GATE
-        _is("g", g, (B, T, HV), torch.float32)
+        _given("g", g, (B, T, HV), f32, index)
     else:
-        _is("g", g, (B, T, HV, dk), torch.float32)
+        _given("g", g, (B, T, HV, dk), f32, index)
     if path.dim() != 2:
         raise ValueError("path must be [B, P]")
     max_path = path.shape[1]
-    _is("path", path, (B, max_path), torch.int32)
-    _is("n_path", n_path, (B,), torch.int32)
+    _given("path", path, (B, max_path), torch.int32, index)
+    _given("n_path", n_path, (B,), torch.int32, index)
+    h0_ptr = None
     if h0 is not None:
-        _is("h0", h0, (B, HV, dk, dv), torch.float32)
+        _given("h0", h0, (B, HV, dk, dv), f32, index)
+        h0_ptr = h0.data_ptr()
     if ht is None:
-        ht = torch.empty(B, HV, dk, dv, dtype=torch.float32, device=dev)
+        ht = torch.empty((B, HV, dk, dv), dtype=f32, device=k.device)
     elif ht is not h0:
-        _is("ht", ht, (B, HV, dk, dv), torch.float32)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    st = lib.gdr_commit_path(k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                             None if h0 is None else h0.data_ptr(), ht.data_ptr(),
-                             path.data_ptr(), n_path.data_ptr(), B, T, HK, HV, dk, dv, max_path,
-                             stream.cuda_stream, code, flags)
-    _check(lib, st)
+        _given("ht", ht, (B, HV, dk, dv), f32, index)
+    st = lib.gdr_commit_path(k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), h0_ptr,
+                             ht.data_ptr(), path.data_ptr(), n_path.data_ptr(), B, T, HK, HV, dk,
+                             dv, max_path, _stream_of(stream, index), code, flags)
+    if st != GDR_OK:
+        _check(lib, st)
     return ht
 
 
@@ -484,44 +481,43 @@ def gdr_state_cache(n_slots, HV, dk, dv, device="cuda"):
             torch.zeros(n_slots, HV, dk, dtype=torch.float32, device=device))
 
 
-def _state_cache_shape(state, slots, cache, scale):
-    if cache.dim() != 4:
-        raise ValueError("cache must be [n_slots, HV, dk, dv]")
+def _state_cache_sizes(slots, cache, scale):
+    """(N, n_slots, HV, dk, dv, device index) of a checked cache and slots."""
+    if cache.dim() != 4 or slots.dim() != 1:
+        raise ValueError("cache must be [n_slots, HV, dk, dv] and slots [N]")
     n_slots, HV, dk, dv = cache.shape
-    N = slots.shape[0] if slots.dim() == 1 else -1
-    _on_device(cache.device, ("cache", cache), ("scale", scale), ("slots", slots),
-               ("state", state))
-    _is("cache", cache, (n_slots, HV, dk, dv), torch.int8)
-    _is("scale", scale, (n_slots, HV, dk), torch.float32)
-    _is("slots", slots, (N,), torch.int32)
-    if state is not None:
-        _is("state", state, (N, HV, dk, dv), torch.float32)
-    return N, n_slots, HV, dk, dv
+    N, index = slots.shape[0], cache.get_device()
+    _given("cache", cache, (n_slots, HV, dk, dv), torch.int8, index)
+    _given("scale", scale, (n_slots, HV, dk), torch.float32, index)
+    _given("slots", slots, (N,), torch.int32, index)
+    return N, n_slots, HV, dk, dv, index
 
 
 def gdr_state_store(state, slots, cache, scale, stream=None):
     """Quantises state [N, HV, dk, dv] f32 into the slots [N] (int32 on the GPU, all different;
     below 0: not stored) of an 8-bit cache (gdr_state_cache)."""
     lib = load_library()
-    N, n_slots, HV, dk, dv = _state_cache_shape(state, slots, cache, scale)
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    _check(lib, lib.gdr_state_store(state.data_ptr(), slots.data_ptr(), cache.data_ptr(),
-                                    scale.data_ptr(), N, n_slots, HV, dk, dv,
-                                    stream.cuda_stream))
+    N, n_slots, HV, dk, dv, index = _state_cache_sizes(slots, cache, scale)
+    _given("state", state, (N, HV, dk, dv), torch.float32, index)
+    st = lib.gdr_state_store(state.data_ptr(), slots.data_ptr(), cache.data_ptr(),
+                             scale.data_ptr(), N, n_slots, HV, dk, dv, _stream_of(stream, index))
+    if st != GDR_OK:
+        _check(lib, st)
 
 
 def gdr_state_load(cache, scale, slots, out=None, stream=None):
     """The states [N, HV, dk, dv] f32 of the slots [N] of an 8-bit cache; zeros for a slot below
     0.  ``out`` is allocated when not given.  Returns it."""
     lib = load_library()
-    N, n_slots, HV, dk, dv = _state_cache_shape(out, slots, cache, scale)
+    N, n_slots, HV, dk, dv, index = _state_cache_sizes(slots, cache, scale)
     if out is None:
-        out = torch.empty(N, HV, dk, dv, dtype=torch.float32, device=cache.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    _check(lib, lib.gdr_state_load(cache.data_ptr(), scale.data_ptr(), slots.data_ptr(),
-                                   out.data_ptr(), N, n_slots, HV, dk, dv, stream.cuda_stream))
+        out = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=cache.device)
+    else:
+        _given("out", out, (N, HV, dk, dv), torch.float32, index)
+    st = lib.gdr_state_load(cache.data_ptr(), scale.data_ptr(), slots.data_ptr(), out.data_ptr(),
+                            N, n_slots, HV, dk, dv, _stream_of(stream, index))
+    if st != GDR_OK:
+        _check(lib, st)
     return out
 
 
