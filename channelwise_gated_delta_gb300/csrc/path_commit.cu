@@ -209,7 +209,7 @@ constexpr int kHalf = kSlotNodes / 2;  // nodes of a slot per producer warp
 // warpgroups.  384 threads are launched with 168 registers each, 64512 in
 // all: 2 x 128 x 200 + 128 x 104.
 constexpr int kBulkThreads = (kGroups + 1) * kGroupWarps * 32;
-constexpr int kStateRegs = 200, kProducerRegs = 104;
+constexpr int kStateRegs = 208, kProducerRegs = 88;
 constexpr uint32_t kStateBytes = kD * kD * 4;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 
@@ -514,9 +514,10 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
             for (int c = 0; c < count; ++c) {
                 const float *kr = &slot.k[c][4 * rg], *ar = &slot.a[c][4 * rg];
                 Pair acc[4];
+                ulonglong2 keys[8];
 #pragma unroll
                 for (int m = 0; m < 8; ++m) {
-                    const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
+                    const ulonglong2 kk = keys[m] = *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
                     const ulonglong2 aa = *reinterpret_cast<const ulonglong2 *>(ar + 16 * m);
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
                 }
 #pragma unroll
                 for (int m = 0; m < 8; ++m) {
-                    const ulonglong2 kk = *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
+                    const ulonglong2 kk = keys[m];
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
