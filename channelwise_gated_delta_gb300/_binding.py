@@ -412,15 +412,15 @@ def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=N
     if max_path is None:
         max_path = T if path is None else path.shape[-1]
     if path is None:
-        path = torch.empty((B, max_path), dtype=i32, device=p.device)
+        path = torch.empty_strided((B, max_path), (max_path, 1), dtype=i32, device=p.device)
     else:
         _given("path", path, (B, max_path), i32, index)
     if n_path is None:
-        n_path = torch.empty(B, dtype=i32, device=p.device)
+        n_path = torch.empty_like(u, dtype=i32)
     else:
         _given("n_path", n_path, (B,), i32, index)
     if next_token is None:
-        next_token = torch.empty(B, dtype=i32, device=p.device)
+        next_token = torch.empty_like(u, dtype=i32)
     else:
         _given("next_token", next_token, (B,), i32, index)
     st = lib.gdr_verify_drafts(p.data_ptr(), q_ptr, tokens.data_ptr(), parent.data_ptr(),
