@@ -30,7 +30,7 @@ namespace {
 constexpr int kMaxNodes = 512;
 constexpr int kMaxVocab = 1 << 22;  // 2^22 weights of at most 2^40 each: sums below 2^63
 constexpr int kMaxCluster = 8;  // the portable limit
-constexpr int kAheadF32 = 4;    // 16-byte loads a lane has in flight per row (bf16: half)
+constexpr int kKeepAhead = 4, kStreamAhead = 8;  // 16-byte loads a lane has in flight per row
 constexpr float kUnit = 1099511627776.f;            // 2^40
 constexpr float kUnitInv = 9.094947017729282e-13f;  // 2^-40
 constexpr int kUBits = 24;
@@ -45,8 +45,7 @@ __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 // low bits of the sum.  floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x)
 // and lo the same of what is left of it.
 struct Mass {
-    uint32_t hi = 0, lo = 0;  // of at most 1024 elements
-    long long sum = 0;
+    uint32_t hi = 0, lo = 0;  // of at most 64 elements: a warp's sums fit 32 bits
     __device__ __forceinline__ void add(float x) {
         constexpr float kTwo20 = 1048576.f, kTwo23 = 8388608.f;
         const float y = __fmul_rn(x, kTwo20);
@@ -55,16 +54,16 @@ struct Mass {
         hi += __float_as_uint(whole) - 0x4b000000u;
         lo += __float_as_uint(__fmaf_rz(rest, kTwo20, kTwo23)) - 0x4b000000u;
     }
-    __device__ __forceinline__ void flush() {
-        sum += ((long long)hi << 20) + lo;
-        hi = lo = 0;
+    __device__ __forceinline__ long long own() const { return ((long long)hi << 20) + lo; }
+    __device__ __forceinline__ long long of_warp() const {
+        const uint32_t h = __reduce_add_sync(0xffffffffu, hi);
+        return ((long long)h << 20) + __reduce_add_sync(0xffffffffu, lo);
     }
 };
 __device__ __forceinline__ long long fix(float x) {
     Mass m;
     m.add(x);
-    m.flush();
-    return m.sum;
+    return m.own();
 }
 __device__ __forceinline__ float mass_of(long long sum) {
     return __fmul_rn(__ll2float_rn(sum), kUnitInv);
@@ -156,44 +155,58 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Stores x to the same variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(long long *var, int rank, long long x) {
+// Stores x to the same variable of CTA `rank` of the cluster and counts its 8
+// bytes on that CTA's barrier.
+__device__ __forceinline__ void store_remote(long long *var, uint64_t *bar, int rank, long long x) {
     asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "st.shared::cluster.b64 [a], %2;\n\t}" ::"r"(sm100::smem_u32(var)),
-        "r"(rank), "l"(x)
+        "{\n\t.reg .b32 a, b;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [a], %3, [b];\n\t}" ::"r"(
+            sm100::smem_u32(var)),
+        "r"(sm100::smem_u32(bar)), "r"(rank), "l"(x)
         : "memory");
 }
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 
-// KEEP: a lane's part of the rows is at most kAhead vectors and stays in
-// registers while the walk is at their node, for further refusals and for the
-// search.  THREADS threads per CTA, 1024 / THREADS CTAs per SM.
-template <typename Tp, bool HAS_Q, bool KEEP, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+// A lane takes its part of the rows in batches of AHEAD 16-byte vectors (of
+// f32; half as many of bf16), whose loads are in flight together.  KEEP > 0:
+// that part is at most KEEP batches and stays in registers while the walk is at
+// their node, for further refusals and for the search.
+template <typename Tp, bool HAS_Q, int KEEP, int THREADS, int AHEAD>
+__global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
     gdr_verify_kernel(const Tp *__restrict__ p, const Tp *__restrict__ q,
                       const int *__restrict__ tokens, const int *__restrict__ parent,
                       const float *__restrict__ coins, const float *__restrict__ u,
                       int *__restrict__ path, int *__restrict__ n_path,
                       int *__restrict__ next_token, int T, int V, long long ldp, long long ldq,
-                      long long parent_sb, long long parent_st, int max_path, int cluster) {
+                      long long parent_sb, long long parent_st, int max_path, int log_cluster,
+                      int *dev_error) {
     constexpr int kThreads = THREADS, kWarps = THREADS / 32;
     constexpr int N = Vec<Tp>::N;
     constexpr int kWide = 32 * N;  // elements of a warp's load: a unit of the row
-    constexpr int kAhead = kAheadF32 * 4 / N;
+    constexpr int kAhead = AHEAD * 4 / N;
     __shared__ int s_parent[kMaxNodes], s_token[kMaxNodes];
+    __shared__ int s_first[kMaxNodes];         // a node's first child
+    __shared__ uint8_t s_first_yes[kMaxNodes];  // whether a node is accepted if it is tried first
     __shared__ float s_coin[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
     __shared__ float s_norm[kMaxNodes];   // with q: the mass of each residual
     __shared__ int s_refused[kMaxNodes];  // without q: the nodes refused
-    __shared__ long long s_warp[kWarps];
+    __shared__ long long s_warp[kWarps], s_before[kWarps];  // a warp's mass, that of those before it
     __shared__ long long s_total[2][kMaxCluster];
+    __shared__ uint64_t s_bar[2];
     __shared__ int s_here, s_out, s_more, s_summed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / cluster, rank = blockIdx.x - b * cluster;
-    cluster_arrive();  // (1) this CTA runs: its shared memory may be written
+    const int b = blockIdx.x >> log_cluster, cluster = 1 << log_cluster;
+    const int rank = blockIdx.x - (b << log_cluster);
+    if (tid < 2) sm100::mbar_init(&s_bar[tid], 1);
+    if (tid == 0) sm100::fence_mbar_init();
+    __syncwarp();
+    cluster_arrive();  // (1) this CTA runs and its barriers are there: others may write to it
 
     // ---- this warp's part of the rows of the node reached
     const Tp *prow = nullptr, *qrow = nullptr;
-    int shift = 0, u0 = 0, u1 = 0, c0 = 0, per_warp = 0, units = 0;
+    int shift = 0, u0 = 0, u1 = 0;
     int f0 = 0, f1 = 0;  // the units whose vectors are aligned and inside the row
     auto take_rows = [&](int node) {
         const size_t row = (size_t)b * T + node;
@@ -205,17 +218,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             qrow = q + row * ldq;
             if (row_shift(qrow) != shift) f1 = f0;
         }
-        units = (V + shift + kWide - 1) / kWide;
-        const int per_cta = (units + cluster - 1) / cluster;
-        per_warp = (per_cta + kWarps - 1) / kWarps;
-        c0 = rank * per_cta;  // this CTA's units: c0 .. min(c0 + per_cta, units) - 1
-        const int c1 = min(c0 + per_cta, units);
+        const int units = (V + shift + kWide - 1) / kWide;
+        const int per_cta = (units + cluster - 1) >> log_cluster;
+        const int per_warp = (per_cta + kWarps - 1) / kWarps;
+        const int c0 = rank * per_cta, c1 = min(c0 + per_cta, units);
         u0 = min(c0 + warp * per_warp, c1);
         u1 = min(u0 + per_warp, c1);
     };
     // the weights of K vectors of a lane; refusals without q are taken off elsewhere
-    auto weights = [&](const auto &pv, const auto &qv, int n, auto &w) {
-        constexpr int K = sizeof(pv) / sizeof(uint4);
+    auto weights = [&](const uint4 *pv, const uint4 *qv, int n, auto &w) {
+        constexpr int M = sizeof(w) / sizeof(float), K = M / N;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float y[N];
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             for (int e = 0; e < N; ++e) w[k * N + e] = probability(y[e]);
         }
         if (HAS_Q && n > 0) {
-            float x[K * N];
+            float x[M];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 float y[N];
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             }
             if (n == 1 && s_norm[0] != 0.f) {  // nearly every row that is read whole
 #pragma unroll
-                for (int e = 0; e < K * N; ++e) w[e] = __saturatef(__fsub_rn(w[e], x[e]));
+                for (int e = 0; e < M; ++e) w[e] = __saturatef(__fsub_rn(w[e], x[e]));
             } else {
                 residuals(w, x, s_norm, n);
             }
@@ -252,102 +264,153 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             if (with_q) qv = load_elements(qrow, i0, V);
         }
     };
-    // the weights of this lane's elements of a unit
-    auto unit_weights = [&](int unit, int n, float (&w)[N]) {
-        uint4 pv[1], qv[1];
-        load_unit(unit, units, HAS_Q && n > 0, pv[0], qv[0]);
-        weights(pv, qv, n, w);
-    };
     // KEEP: the rows of node `held`
-    uint4 kept_p[KEEP ? kAhead : 1], kept_q[KEEP ? kAhead : 1];
+    constexpr int kKept = KEEP > 0 ? KEEP * kAhead : 1;
+    uint4 kept_p[kKept], kept_q[kKept];
     int held = -1;
     auto hold = [&](int node) {
-        if (!KEEP || node == held) return;
+        if (KEEP == 0 || node == held) return;
         held = node;
         take_rows(node);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) load_unit(u0 + k, u1, HAS_Q, kept_p[KEEP ? k : 0], kept_q[KEEP ? k : 0]);
+        for (int k = 0; k < kKept; ++k) load_unit(u0 + k, u1, HAS_Q, kept_p[k], kept_q[k]);
     };
-    // mass of units lo .. hi - 1 after n refusals, in every lane of the warp
-    auto mass = [&](int lo, int hi, int n) -> long long {
+    // Mass of this warp's units after n refusals, in every lane.  Lane i also
+    // keeps that of the i-th group of per_group batches of kAhead units, for the search.
+    long long group = 0;
+    int per_group = 1;
+    auto add_all = [&](const auto &w) {
+        constexpr int M = sizeof(w) / sizeof(float);
         Mass part;
-        if (KEEP) {  // lo .. hi - 1 are this warp's own units
-            float w[(KEEP ? kAhead : 1) * N];
-            weights(kept_p, kept_q, n, w);
 #pragma unroll
-            for (int e = 0; e < (KEEP ? kAhead : 1) * N; ++e) part.add(w[e]);
-            part.flush();
+        for (int e = 0; e < M; ++e) part.add(w[e]);
+        return part;
+    };
+    auto mass = [&](int n) -> long long {
+        const int batches = (u1 - u0 + kAhead - 1) / kAhead;
+        per_group = max(1, (batches + 31) / 32);
+        group = 0;
+        if constexpr (KEEP > 0) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i) {
+                float w[kAhead * N];
+                weights(kept_p + i * kAhead, kept_q + i * kAhead, n, w);
+                const long long sum = add_all(w).of_warp();
+                if (lane == i) group = sum;
+            }
         }
-        for (int at = lo; !KEEP && at < hi; at += kAhead) {
+        for (int i = 0, to = 0, left = per_group; KEEP == 0 && i < batches; ++i) {
+            const int at = u0 + i * kAhead;
             uint4 pv[kAhead], qv[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const bool whole = at + k < hi && at + k >= f0 && at + k < f1;
+                const bool whole = at + k < u1 && at + k >= f0 && at + k < f1;
                 const int i0 = (at + k) * kWide + lane * N - shift;
                 pv[k] = whole ? load_vec(prow, i0) : make_uint4(0u, 0u, 0u, 0u);
                 qv[k] = HAS_Q && n > 0 && whole ? load_vec(qrow, i0) : make_uint4(0u, 0u, 0u, 0u);
             }
-            if (at < f0 || min(at + kAhead, hi) > f1) {  // the ends of the row, one by one
+            long long sum = 0;
+            if (at < f0 || min(at + kAhead, u1) > f1) {  // the ends of the row, one by one
                 for (int k = 0; k < kAhead; ++k) {
-                    if (at + k >= hi || (at + k >= f0 && at + k < f1)) continue;
+                    if (at + k >= u1 || (at + k >= f0 && at + k < f1)) continue;
+                    uint4 ep, eq;
+                    load_unit(at + k, u1, HAS_Q && n > 0, ep, eq);
                     float w[N];
-                    unit_weights(at + k, n, w);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) part.add(w[e]);
+                    weights(&ep, &eq, n, w);
+                    sum += add_all(w).of_warp();
                 }
             }
             float w[kAhead * N];
             weights(pv, qv, n, w);
-#pragma unroll
-            for (int e = 0; e < kAhead * N; ++e) part.add(w[e]);
-            part.flush();
+            sum += add_all(w).of_warp();
+            if (lane == to) group += sum;
+            if (--left == 0) {
+                left = per_group;
+                ++to;
+            }
         }
         if (!HAS_Q)
-            for (int s = lane; s < n; s += 32) {
+            for (int s = 0; s < n; ++s) {
                 const int unit = (s_token[s_refused[s]] + shift) / kWide;
-                if (unit >= lo && unit < hi) part.sum -= fix(s_p[s_refused[s]]);
+                if (unit >= u0 && unit < u1 && lane == (unit - u0) / kAhead / per_group)
+                    group -= fix(s_p[s_refused[s]]);
             }
-        return warp_sum(part.sum);
+        return warp_sum(group);
     };
-    if (KEEP) hold(0);  // in flight with the nodes: the walk may well end at the root
-    for (int t = tid; t < T; t += kThreads) {
-        const size_t at = (size_t)b * T + t;
-        int par = -1, tok = -1;
-        if (t > 0) {
-            par = parent[b * parent_sb + t * parent_st];
-            tok = tokens[at];
+    // ---- the nodes, every CTA for itself: this thread's first one is loaded
+    // at once, the others (T > kThreads) after it
+    const float uu = u[b];
+    const int *my_parent = parent + b * parent_sb;
+    auto node_of = [&](int t, int &par, int &tok, float &coin) {
+        par = tok = -1;
+        coin = 0.f;
+        if (t > 0 && t < T) {
+            par = my_parent[t * parent_st];
+            tok = tokens[(size_t)b * T + t];
+            coin = coins[(size_t)b * T + t];
         }
-        const float coin = coins[at];
+    };
+    int par, tok;
+    float coin;
+    node_of(tid, par, tok, coin);
+    if (KEEP > 0) hold(0);  // in flight with the nodes: the walk may well end at the root
+    for (int t = tid; t < T; t += kThreads) s_first[t] = T;
+    __syncthreads();
+    for (int t = tid; t < T; t += kThreads) {
+        if (t != tid) node_of(t, par, tok, coin);
         const bool ok = par >= 0 && par < t && tok >= 0 && tok < V;
         const size_t row = (size_t)b * T + (ok ? par : 0);
-        s_p[t] = ok ? probability(to_f32(p[row * ldp + tok])) : 0.f;
-        s_q[t] = ok && HAS_Q ? probability(to_f32(q[row * ldq + tok])) : 0.f;
+        const float P = ok ? probability(to_f32(p[row * ldp + tok])) : 0.f;
+        const float Q = ok && HAS_Q ? probability(to_f32(q[row * ldq + tok])) : 0.f;
+        if (ok) atomicMin(&s_first[par], t);
+        s_first_yes[t] = P > 0.f && __fmul_rn(coin, HAS_Q ? Q : 1.f) < P;
+        s_p[t] = P;
+        s_q[t] = Q;
         s_parent[t] = ok ? par : -1;
         s_token[t] = tok;
         s_coin[t] = coin;
     }
-    const float uu = u[b];
     __syncthreads();
 
     int round = 0;
-    // total mass of the node's rows after n refusals; each warp's in s_warp,
-    // each CTA's in s_total[round & 1]
+    bool ok = true;
+    long long before = 0;  // mass of the CTAs before this one
+    // Total mass of the node's rows after n refusals.  Each CTA's goes to all
+    // others; round r's barrier and totals are used again in round r + 2, which
+    // no CTA enters before every other one has left round r.
     auto total_mass = [&](int n) -> long long {
-        const long long mine = mass(u0, u1, n);
+        const long long mine = mass(n);
         if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
         ++round;
         long long *totals = s_total[round & 1];
+        uint64_t *bar = &s_bar[round & 1];
         if (round == 1) cluster_wait();  // (1)
+        bool got = true;
         if (warp == 0) {
-            const long long all = warp_sum(lane < kWarps ? s_warp[lane] : 0);
-            if (lane < cluster) store_remote(totals + rank, lane, all);
+            const long long own = lane < kWarps ? s_warp[lane] : 0;
+            long long upto = own;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += y;
+            }
+            if (lane < kWarps) s_before[lane] = upto - own;
+            const long long all = __shfl_sync(0xffffffffu, upto, 31);
+            if (lane == 0) sm100::mbar_arrive_expect_tx(bar, 8 * cluster);
             __syncwarp();
+            if (lane < cluster) store_remote(totals + rank, bar, lane, all);
+            got = sm100::mbar_wait_bounded(bar, (uint32_t)(round - 1) >> 1 & 1u, kWaitNs);
         }
-        cluster_arrive();
-        cluster_wait();
+        ok = __syncthreads_and(got) != 0;
         long long sum = 0;
-        for (int r = 0; r < cluster; ++r) sum += totals[r];
+        before = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            const long long x = r < cluster ? totals[r] : 0;
+            sum += x;
+            if (r < rank) before += x;
+        }
         return sum;
     };
 
@@ -364,16 +427,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         if (warp == 0) {
             bool more = false;
             while (n < max_path) {
-                // the next child of `here` behind node `tried`
+                // first children one after the other, as far as they are accepted
                 int t = T;
-                for (int base = (tried + 1) & ~31; base < T; base += 32) {
+                if (out == 0 && tried == here) {
+                    t = s_first[here];
+                    if (t < T && s_first_yes[t]) {
+                        here = tried = t;
+                        summed = false;
+                        if (writer) my_path[n] = t;
+                        ++n;
+                        continue;
+                    }
+                }
+                // the next child of `here` behind node `tried`
+                for (int base = (tried + 1) & ~31; t == T && base < T; base += 32) {
                     const int at = base + lane;
                     const unsigned hit = __ballot_sync(
                         0xffffffffu, at > tried && at < T && s_parent[min(at, T - 1)] == here);
-                    if (hit) {
-                        t = base + __ffs(hit) - 1;
-                        break;
-                    }
+                    if (hit) t = base + __ffs(hit) - 1;
                 }
                 if (t >= T) break;
                 tried = t;
@@ -423,11 +494,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         out = s_out;
         summed = s_summed;
         if (!HAS_Q || !s_more) break;
-        if (KEEP)
+        if (KEEP > 0)
             hold(here);
         else
             take_rows(here);
         total = total_mass(out);
+        if (!ok) break;
         summed = total > 0;  // without mass the weights stay those of before
         if (tid == 0) s_norm[out - 1] = mass_of(total);
         __syncthreads();
@@ -438,16 +510,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     }
 
     // ---- the next token
-    if (!HAS_Q || !summed) {
-        if (KEEP)
+    if (ok && (!HAS_Q || !summed)) {
+        if (KEEP > 0)
             hold(here);
         else
             take_rows(here);
         total = total_mass(out);
     }
-    if (!HAS_Q && total == 0 && out > 0) {  // nothing left: the row as it was
+    if (!HAS_Q && ok && total == 0 && out > 0) {  // nothing left: the row as it was
         out = 0;
         total = total_mass(0);
+    }
+    if (!ok) {  // a total did not come: never leave with others' stores on their way here
+        if (tid == 0) {
+            atomicOr(dev_error, 1);
+            sm100::mbar_wait_bounded(&s_bar[round & 1], (uint32_t)(round - 1) >> 1 & 1u, kWaitNs);
+        }
+        return;
     }
     if (total == 0) {
         if (writer) next_token[b] = -1;
@@ -457,73 +536,78 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     const long long m = (long long)__fmul_rn(fminf(fmaxf(uu, 0.f), top), (float)(1 << kUBits));
     const long long low = (1 << kUBits) - 1;
     long long goal = (total >> kUBits) * m + (((total & low) * m) >> kUBits);  // floor(total m / 2^24)
-    const long long *totals = s_total[round & 1];
-    for (int r = 0; r < rank; ++r) goal -= totals[r];
-    if (goal < 0 || goal >= totals[rank]) return;
-    int w = 0;
-    for (; goal >= s_warp[w]; ++w) goal -= s_warp[w];
-    // looks for the goal among a unit's elements, of weights x; takes the unit's mass off it
-    auto in_unit = [&](int unit, float (&x)[N]) -> bool {
-        const int i0 = unit * kWide + lane * N - shift;
-        if (!HAS_Q)
-            for (int s = 0; s < out; ++s) {
-                const int e = s_token[s_refused[s]] - i0;
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (k == e) x[k] = 0.f;
-            }
-        Mass own;
-#pragma unroll
-        for (int e = 0; e < N; ++e) own.add(x[e]);
-        own.flush();
-        long long upto = own.sum;  // of the lanes up to this one
+    goal -= before + s_before[warp];
+    if (goal < 0 || goal >= s_warp[warp]) return;  // in another warp's part
+    // the group of batches, the batch, the unit, the lane, the element
+    long long upto = group;  // of the lanes up to this one
+    auto scan = [&]() {
+        const long long own = upto;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += y;
         }
-        if (upto - own.sum <= goal && goal < upto) {
-            long long run = upto - own.sum;
+        return own;
+    };
+    const long long mine = scan();
+    const int to = __ffs(__ballot_sync(0xffffffffu, goal < upto)) - 1;
+    goal -= __shfl_sync(0xffffffffu, upto - mine, to);
+    // a batch from unit `at` on; whether the goal was in it, else its mass is taken off the goal
+    auto in_batch = [&](int at, const uint4 *pv, const uint4 *qv) -> bool {
+        float x[kAhead * N];
+        weights(pv, qv, out, x);
+        const int i0 = at * kWide + lane * N - shift;  // of the first unit
+        if (!HAS_Q)
+            for (int s = 0; s < out; ++s) {
+                const int gone = s_token[s_refused[s]] - i0;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (gone == k * kWide + e) x[k * N + e] = 0.f;
+            }
+        int unit = -1;
+        float y[N] = {};
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            Mass part;
+#pragma unroll
+            for (int e = 0; e < N; ++e) part.add(x[k * N + e]);
+            const long long sum = part.of_warp();
+            if (unit < 0 && goal < sum) {
+                unit = k;
+                upto = part.own();
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[e] = x[k * N + e];
+            }
+            if (unit < 0) goal -= sum;
+        }
+        if (unit < 0) return false;
+        const long long own = scan();
+        long long run = upto - own;  // of the lanes before this one
+        if (run <= goal && goal < upto) {
             int found = -1;  // the first element whose running sum is above
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                run += fix(x[e]);
+                run += fix(y[e]);
                 if (found < 0 && run > goal) found = e;
             }
-            next_token[b] = i0 + found;
+            next_token[b] = i0 + unit * kWide + found;
         }
-        const long long all = __shfl_sync(0xffffffffu, upto, 31);
-        const bool hit = goal < all;
-        goal -= all;
-        return hit;
+        return true;
     };
-    if (KEEP) {
-        if (w != warp) return;
+    if constexpr (KEEP > 0) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const uint4 pv[1] = {kept_p[KEEP ? k : 0]}, qv[1] = {kept_q[KEEP ? k : 0]};
-            float x[N];
-            weights(pv, qv, out, x);
-            if (in_unit(u0 + k, x)) return;
-        }
+        for (int i = 0; i < KEEP; ++i)
+            if (i == to) in_batch(u0 + i * kAhead, kept_p + i * kAhead, kept_q + i * kAhead);
         return;
     }
-    // the warp's units divided among all warps of the CTA, then one by one
-    const int per_cta = (units + cluster - 1) / cluster, c1 = min(c0 + per_cta, units);
-    const int w0 = min(c0 + w * per_warp, c1), w1 = min(w0 + per_warp, c1);
-    const int step = (w1 - w0 + kWarps - 1) / kWarps;
-    const int m0 = min(w0 + warp * step, w1), m1 = min(m0 + step, w1);
-    __syncthreads();
-    const long long mine = mass(m0, m1, out);
-    if (lane == 0) s_warp[warp] = mine;
-    __syncthreads();
-    w = 0;
-    for (; goal >= s_warp[w]; ++w) goal -= s_warp[w];
-    if (w != warp) return;
-    for (int at = m0; at < m1; ++at) {
-        float x[N];
-        unit_weights(at, out, x);
-        if (in_unit(at, x)) return;
+    for (int at = u0 + to * per_group * kAhead; at < u1; at += kAhead) {
+        uint4 pv[kAhead], qv[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            load_unit(at + k, u1, HAS_Q && out > 0, pv[k], qv[k]);
+        if (in_batch(at, pv, qv)) return;
     }
 }
 
@@ -537,8 +621,12 @@ struct VerifyArgs {
     int max_path;
 };
 
-template <typename Tp, bool HAS_Q, bool KEEP, int THREADS>
+template <typename Tp, bool HAS_Q, int KEEP, int THREADS, int AHEAD>
 cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
+    int *err = nullptr, log_c = 0;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    while (1 << log_c < c) ++log_c;
     if ((long long)a.B * c > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -551,10 +639,10 @@ cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     trace_begin(kKernVerify, stream);
-    const cudaError_t e = cudaLaunchKernelEx(
-        &cfg, gdr_verify_kernel<Tp, HAS_Q, KEEP, THREADS>, static_cast<const Tp *>(a.p),
+    e = cudaLaunchKernelEx(
+        &cfg, gdr_verify_kernel<Tp, HAS_Q, KEEP, THREADS, AHEAD>, static_cast<const Tp *>(a.p),
         static_cast<const Tp *>(a.q), a.tokens, a.parent, a.coins, a.u, a.path, a.n_path,
-        a.next_token, a.T, a.V, a.ldp, a.ldq, a.parent_sb, a.parent_st, a.max_path, c);
+        a.next_token, a.T, a.V, a.ldp, a.ldq, a.parent_sb, a.parent_st, a.max_path, log_c, err);
     trace_end(kKernVerify, stream);
     return e;
 }
@@ -564,30 +652,31 @@ cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
 // with the fewest threads whose lanes can keep their part of the row.  Clusters
 // of 8 do not fill the device (a cluster keeps to one processing cluster of
 // SMs), so 7 of 8 SMs are counted.  Otherwise CTAs of 256 threads that stream
-// the rows, doubled while the trees' CTAs would leave the device's slots (4
-// a SM) empty and each would keep 1024 elements.
+// the rows, doubled while the trees' CTAs would leave the device's slots (2
+// a SM) empty and each would keep 2048 elements.
 template <typename Tp, bool HAS_Q>
 cudaError_t launch_q(const VerifyArgs &a, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    constexpr int N = Vec<Tp>::N, kKeep = kAheadF32 * 4 / N;
+    constexpr int N = Vec<Tp>::N, kBatch = kKeepAhead * 4 / N;  // units
     int c = 1;
     while (c < kMaxCluster && (long long)a.B * 2 * c <= sms * 7 / 8 && a.V >= 2 * c * 256 * N)
         c *= 2;
     if (a.B <= sms) {
         // the units of a warp, of a row that may begin anywhere in a vector
         const int units = (a.V + N - 1 + 32 * N - 1) / (32 * N), per_cta = (units + c - 1) / c;
-        if ((per_cta + 7) / 8 <= kKeep) return launch_clusters<Tp, HAS_Q, true, 256>(a, c, stream);
-        if ((per_cta + 15) / 16 <= kKeep)
-            return launch_clusters<Tp, HAS_Q, true, 512>(a, c, stream);
-        if ((per_cta + 31) / 32 <= kKeep)
-            return launch_clusters<Tp, HAS_Q, true, 1024>(a, c, stream);
+        if ((per_cta + 7) / 8 <= kBatch)
+            return launch_clusters<Tp, HAS_Q, 1, 256, kKeepAhead>(a, c, stream);
+        if ((per_cta + 15) / 16 <= kBatch)
+            return launch_clusters<Tp, HAS_Q, 1, 512, kKeepAhead>(a, c, stream);
+        if ((per_cta + 15) / 16 <= 2 * kBatch)
+            return launch_clusters<Tp, HAS_Q, 2, 512, kKeepAhead>(a, c, stream);
     }
     c = 1;
-    while (c < kMaxCluster && (long long)a.B * c < 4LL * sms && a.V / (2 * c) >= 1024) c *= 2;
-    return launch_clusters<Tp, HAS_Q, false, 256>(a, c, stream);
+    while (c < kMaxCluster && (long long)a.B * 2 * c <= 2LL * sms && a.V / (2 * c) >= 2048) c *= 2;
+    return launch_clusters<Tp, HAS_Q, 0, 256, kStreamAhead>(a, c, stream);
 }
 
 // Whether `rows` rows `ld` apart are addressable (element offsets below 2^58).
