@@ -600,14 +600,14 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
             if (i == to) in_batch(u0 + i * kAhead, kept_p + i * kAhead, kept_q + i * kAhead);
-        return;
-    }
-    for (int at = u0 + to * per_group * kAhead; at < u1; at += kAhead) {
-        uint4 pv[kAhead], qv[kAhead];
+    } else {
+        for (int at = u0 + to * per_group * kAhead; at < u1; at += kAhead) {
+            uint4 pv[kAhead], qv[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            load_unit(at + k, u1, HAS_Q && out > 0, pv[k], qv[k]);
-        if (in_batch(at, pv, qv)) return;
+            for (int k = 0; k < kAhead; ++k)
+                load_unit(at + k, u1, HAS_Q && out > 0, pv[k], qv[k]);
+            if (in_batch(at, pv, qv)) return;
+        }
     }
 }
 

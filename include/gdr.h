@@ -390,8 +390,8 @@ GDR_API gdr_status gdr_forward_tree(const void *q, const void *k, const void *v,
  *               the target's distribution of the token after node t
  *   q           the draft's, rows ldq elements apart: row (b, t) is the
  *               distribution that the children of node t were drawn from,
- *               each by itself (rows of nodes without children are not
- *               read).  NULL: the children were proposed, not drawn
+ *               each by itself (what a row of a node without children holds
+ *               does not matter).  NULL: the children were proposed, not drawn
  *   tokens      int32 [B][T] token of each node (node 0's is not read)
  *   parent      int32, of node t of tree b at parent[b * parent_sb + t * parent_st]
  *               (a packed [B][T]: T and 1; one tree shape for the whole batch:
