@@ -170,11 +170,11 @@ __device__ __forceinline__ void store_remote(long long *var, uint64_t *bar, int 
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 
 // A lane takes its part of the rows in batches of AHEAD 16-byte vectors (of
-// f32; half as many of bf16), whose loads are in flight together.  KEEP > 0:
-// that part is at most KEEP batches and stays in registers while the walk is at
-// their node, for further refusals and for the search.
-template <typename Tp, bool HAS_Q, int KEEP, int THREADS, int AHEAD>
-__global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
+// f32; half as many of bf16), whose loads are in flight together.  KEEP: that
+// part is one batch at most and stays in registers while the walk is at its
+// node, for further refusals and for the search.
+template <typename Tp, bool HAS_Q, bool KEEP, int THREADS, int AHEAD>
+__global__ void __launch_bounds__(THREADS, KEEP ? 1 : 2)
     gdr_verify_kernel(const Tp *__restrict__ p, const Tp *__restrict__ q,
                       const int *__restrict__ tokens, const int *__restrict__ parent,
                       const float *__restrict__ coins, const float *__restrict__ u,
@@ -265,15 +265,14 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
         }
     };
     // KEEP: the rows of node `held`
-    constexpr int kKept = KEEP > 0 ? KEEP * kAhead : 1;
-    uint4 kept_p[kKept], kept_q[kKept];
+    uint4 kept_p[kAhead], kept_q[kAhead];
     int held = -1;
     auto hold = [&](int node) {
-        if (KEEP == 0 || node == held) return;
+        if (node == held) return;
         held = node;
         take_rows(node);
 #pragma unroll
-        for (int k = 0; k < kKept; ++k) load_unit(u0 + k, u1, HAS_Q, kept_p[k], kept_q[k]);
+        for (int k = 0; k < kAhead; ++k) load_unit(u0 + k, u1, HAS_Q, kept_p[k], kept_q[k]);
     };
     // Mass of this warp's units after n refusals, in every lane.  Lane i also
     // keeps that of the i-th group of per_group batches of kAhead units, for the search.
@@ -290,16 +289,13 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
         const int batches = (u1 - u0 + kAhead - 1) / kAhead;
         per_group = max(1, (batches + 31) / 32);
         group = 0;
-        if constexpr (KEEP > 0) {
-#pragma unroll
-            for (int i = 0; i < KEEP; ++i) {
-                float w[kAhead * N];
-                weights(kept_p + i * kAhead, kept_q + i * kAhead, n, w);
-                const long long sum = add_all(w).of_warp();
-                if (lane == i) group = sum;
-            }
+        if constexpr (KEEP) {
+            float w[kAhead * N];
+            weights(kept_p, kept_q, n, w);
+            const long long sum = add_all(w).of_warp();
+            if (lane == 0) group = sum;
         }
-        for (int i = 0, to = 0, left = per_group; KEEP == 0 && i < batches; ++i) {
+        for (int i = 0, to = 0, left = per_group; !KEEP && i < batches; ++i) {
             const int at = u0 + i * kAhead;
             uint4 pv[kAhead], qv[kAhead];
 #pragma unroll
@@ -353,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
     int par, tok;
     float coin;
     node_of(tid, par, tok, coin);
-    if (KEEP > 0) hold(0);  // in flight with the nodes: the walk may well end at the root
+    if (KEEP) hold(0);  // in flight with the nodes: the walk may well end at the root
     for (int t = tid; t < T; t += kThreads) s_first[t] = T;
     __syncthreads();
     for (int t = tid; t < T; t += kThreads) {
@@ -494,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
         out = s_out;
         summed = s_summed;
         if (!HAS_Q || !s_more) break;
-        if (KEEP > 0)
+        if (KEEP)
             hold(here);
         else
             take_rows(here);
@@ -511,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
 
     // ---- the next token
     if (ok && (!HAS_Q || !summed)) {
-        if (KEEP > 0)
+        if (KEEP)
             hold(here);
         else
             take_rows(here);
@@ -596,10 +592,8 @@ __global__ void __launch_bounds__(THREADS, KEEP > 0 ? 1 : 2)
         }
         return true;
     };
-    if constexpr (KEEP > 0) {
-#pragma unroll
-        for (int i = 0; i < KEEP; ++i)
-            if (i == to) in_batch(u0 + i * kAhead, kept_p + i * kAhead, kept_q + i * kAhead);
+    if constexpr (KEEP) {
+        in_batch(u0, kept_p, kept_q);
     } else {
         for (int at = u0 + to * per_group * kAhead; at < u1; at += kAhead) {
             uint4 pv[kAhead], qv[kAhead];
@@ -621,7 +615,7 @@ struct VerifyArgs {
     int max_path;
 };
 
-template <typename Tp, bool HAS_Q, int KEEP, int THREADS, int AHEAD>
+template <typename Tp, bool HAS_Q, bool KEEP, int THREADS, int AHEAD>
 cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
     int *err = nullptr, log_c = 0;
     cudaError_t e = device_error_word(&err);
@@ -647,13 +641,21 @@ cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
     return e;
 }
 
-// CTAs per tree, a power of two up to the cluster limit.  Few trees: as many
-// as SMs and row allow (a CTA has a vector at least for each of 256 threads),
-// with the fewest threads whose lanes can keep their part of the row.  Clusters
-// of 8 do not fill the device (a cluster keeps to one processing cluster of
-// SMs), so 7 of 8 SMs are counted.  Otherwise CTAs of 256 threads that stream
-// the rows, doubled while the trees' CTAs would leave the device's slots (2
-// a SM) empty and each would keep 2048 elements.
+// CTAs per tree (a power of two up to the cluster limit) and variant, by the
+// number of trees and the length of a row.  Figures: us on the device, chains
+// of 8 nodes, f32 with q.
+// Where a lane's part of the row fits one batch, it is kept, with the fewest
+// threads that suffice: 32,000 elements, one tree: 4.8 kept by 256 threads, 5.3 by 512, 6.0
+// streamed; 60,000: 5.4 kept by 512, 6.5 streamed.  (Two batches a lane kept:
+// 7.0 at 131,072 elements, the same as streamed.)  There every tree gets as
+// many CTAs as SMs and row allow (32,000 elements, one tree: 8.6 / 6.6 / 5.5 /
+// 4.8 with 1 / 2 / 4 / 8), each with a vector at least for each of 256 threads.
+// Clusters of 8 do not fill the device (a cluster keeps to one processing
+// cluster of SMs): 7 of 8 SMs are counted (2,000 elements, 64 trees: 10.3
+// with 8 CTAs each, 5.6 with 1).
+// Otherwise CTAs of 256 threads, two a SM, stream the rows, as many per tree as
+// fit the device at once with 2048 elements each (131,072 elements, 64 trees: 25.3 / 18.2 / 16.4 /
+// 20.7 with 1 / 2 / 4 / 8; one tree: 17.6 / 11.9 / 8.7 / 7.0).
 template <typename Tp, bool HAS_Q>
 cudaError_t launch_q(const VerifyArgs &a, cudaStream_t stream) {
     int dev = 0, sms = 0;
@@ -668,15 +670,13 @@ cudaError_t launch_q(const VerifyArgs &a, cudaStream_t stream) {
         // the units of a warp, of a row that may begin anywhere in a vector
         const int units = (a.V + N - 1 + 32 * N - 1) / (32 * N), per_cta = (units + c - 1) / c;
         if ((per_cta + 7) / 8 <= kBatch)
-            return launch_clusters<Tp, HAS_Q, 1, 256, kKeepAhead>(a, c, stream);
+            return launch_clusters<Tp, HAS_Q, true, 256, kKeepAhead>(a, c, stream);
         if ((per_cta + 15) / 16 <= kBatch)
-            return launch_clusters<Tp, HAS_Q, 1, 512, kKeepAhead>(a, c, stream);
-        if ((per_cta + 15) / 16 <= 2 * kBatch)
-            return launch_clusters<Tp, HAS_Q, 2, 512, kKeepAhead>(a, c, stream);
+            return launch_clusters<Tp, HAS_Q, true, 512, kKeepAhead>(a, c, stream);
     }
     c = 1;
     while (c < kMaxCluster && (long long)a.B * 2 * c <= 2LL * sms && a.V / (2 * c) >= 2048) c *= 2;
-    return launch_clusters<Tp, HAS_Q, 0, 256, kStreamAhead>(a, c, stream);
+    return launch_clusters<Tp, HAS_Q, false, 256, kStreamAhead>(a, c, stream);
 }
 
 // Whether `rows` rows `ld` apart are addressable (element offsets below 2^58).

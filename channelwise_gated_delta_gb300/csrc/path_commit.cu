@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kNodes = 8;      // nodes staged at a time
 constexpr int kWarpCols = 16;  // columns of a warp
+constexpr int kCols = 32;      // of a CTA
 
 struct Pair {
     unsigned long long v;
@@ -58,15 +59,17 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
     return r;
 }
 
-// One CTA: BV columns of one head (BV / 16 warps).
-template <typename Tin, int DK, int BV, bool GS>
-__global__ void __launch_bounds__(2 * BV, (DK == 128 ? 3 : 4) * 64 / BV)
+// One CTA: kCols columns of one head, two warps.  (Four warps, which stage k
+// and exp(g) half as often: 2 x 32 heads of 64 x 64, paths of up to 6 nodes, 3.3 us either way; 64 x 32
+// heads 18.3 against 18.6, of 128 x 64 31.4 against 31.5.)
+template <typename Tin, int DK, bool GS>
+__global__ void __launch_bounds__(2 * kCols, DK == 128 ? 6 : 8)
     gdr_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v,
                       const float *__restrict__ g, const float *__restrict__ beta,
                       const float *h0, float *ht, const int *__restrict__ path,
                       const int *__restrict__ n_path, int T, int HK, int HV, int dv,
                       int max_path) {
-    constexpr int NT = 2 * BV, RM = DK / 8;
+    constexpr int BV = kCols, NT = 2 * BV, RM = DK / 8;
     __shared__ float4 s_ka[kNodes][DK];  // k, k, a, a
     __shared__ float s_v[kNodes][BV];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -584,22 +587,12 @@ struct CommitArgs {
     int B, T, HK, HV, dk, dv, max_path;
 };
 
-template <typename Tin, int DK, int BV, bool GS>
-cudaError_t launch_bv(const CommitArgs &a, cudaStream_t stream) {
-    const long long ctas = (long long)a.B * a.HV * (a.dv / BV);
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    trace_begin(kKernCommit, stream);
-    gdr_commit_kernel<Tin, DK, BV, GS><<<(unsigned)ctas, 2 * BV, 0, stream>>>(
-        static_cast<const Tin *>(a.k), static_cast<const Tin *>(a.v), a.g, a.beta, a.h0, a.ht,
-        a.path, a.n_path, a.T, a.HK, a.HV, a.dv, a.max_path);
-    trace_end(kKernCommit, stream);
-    return cudaGetLastError();
-}
-
 template <typename Tin, bool GS>
-cudaError_t launch_bulk(const CommitArgs &a, int sms, cudaStream_t stream) {
-    int *err = nullptr;
+cudaError_t launch_bulk(const CommitArgs &a, cudaStream_t stream) {
+    int *err = nullptr, dev = 0, sms = 0;
     cudaError_t e = device_error_word(&err);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int nheads = a.B * a.HV;  // at most 2^30
     const int grid = nheads < sms ? nheads : sms;
@@ -615,22 +608,21 @@ cudaError_t launch_bulk(const CommitArgs &a, int sms, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// 64 columns per CTA, so that k and exp(g) are staged twice a head; 32 where
-// dv is 32 or where 64 would give fewer CTAs than the device has SMs.
 template <typename Tin, int DK, bool GS>
 cudaError_t launch(const CommitArgs &a, cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    if (DK == kD && a.dv == kD) return launch_bulk<Tin, GS>(a, sms, stream);
-    if (a.dv < 64 || (long long)a.B * a.HV * (a.dv / 64) < sms)
-        return launch_bv<Tin, DK, 32, GS>(a, stream);
-    return launch_bv<Tin, DK, 64, GS>(a, stream);
+    const long long ctas = (long long)a.B * a.HV * (a.dv / kCols);
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    trace_begin(kKernCommit, stream);
+    gdr_commit_kernel<Tin, DK, GS><<<(unsigned)ctas, 2 * kCols, 0, stream>>>(
+        static_cast<const Tin *>(a.k), static_cast<const Tin *>(a.v), a.g, a.beta, a.h0, a.ht,
+        a.path, a.n_path, a.T, a.HK, a.HV, a.dv, a.max_path);
+    trace_end(kKernCommit, stream);
+    return cudaGetLastError();
 }
 
 template <typename Tin, bool GS>
 cudaError_t launch_dk(const CommitArgs &a, cudaStream_t stream) {
+    if (a.dk == kD && a.dv == kD) return launch_bulk<Tin, GS>(a, stream);
     switch (a.dk) {
         case 32: return launch<Tin, 32, GS>(a, stream);
         case 64: return launch<Tin, 64, GS>(a, stream);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 template <int DV>
 cudaError_t launch_store(const float *state, const int *slots, signed char *cache, float *scale,
                          int N, int n_slots, int HV, int dk, cudaStream_t stream) {
-    const unsigned state_warps = (unsigned)(HV * dk / Rows<DV>::kWarpRows);
+    const unsigned state_warps = (unsigned)((long long)HV * dk / Rows<DV>::kWarpRows);
     const unsigned warps = (unsigned)N * state_warps;  // at most 2^30 (check())
     trace_begin(kKernStateStore, stream);
     gdr_state_store_kernel<DV><<<(warps + kWarps - 1) / kWarps, 32 * kWarps, 0, stream>>>(
@@ -154,7 +154,7 @@ cudaError_t launch_store(const float *state, const int *slots, signed char *cach
 template <int DV>
 cudaError_t launch_load(const signed char *cache, const float *scale, const int *slots,
                         float *state, int N, int n_slots, int HV, int dk, cudaStream_t stream) {
-    const unsigned state_warps = (unsigned)(HV * dk / Rows<DV>::kWarpRows);
+    const unsigned state_warps = (unsigned)((long long)HV * dk / Rows<DV>::kWarpRows);
     const unsigned warps = (unsigned)N * state_warps;  // at most 2^30 (check())
     trace_begin(kKernStateLoad, stream);
     gdr_state_load_kernel<DV><<<(warps + kWarps - 1) / kWarps, 32 * kWarps, 0, stream>>>(

@@ -98,6 +98,16 @@ def test_decay_from_slow_to_everything(mu):
     check(draw(2, 9, 2, 4, 128, 128, dtype=torch.bfloat16, seed=5, g_mu=mu), *paths(2, 9, 9, 1))
 
 
+@pytest.mark.parametrize("dims", [(128, 128), (64, 32)])
+def test_channels_that_forget_everything(dims):
+    """g = -inf: exp(g) = 0 and the row starts again; beta = 0: the node only decays."""
+    d = draw(2, 8, 1, 2, *dims, seed=13)
+    d["g"][:, 2, :, ::3] = float("-inf")
+    d["g"][1, 4] = float("-inf")
+    d["beta"][:, 5] = 0.0
+    check(d, *paths(2, 8, 8, lengths=[8]))
+
+
 def test_state_grows_where_the_gate_lets_it():
     d = draw(2, 5, 1, 2, 64, 64, seed=6)
     d["g"] = d["g"].abs() * 0.1
