@@ -16,7 +16,13 @@
 // the bandwidth of the rows.  A tree is therefore one cluster of CTAs, each
 // of which walks the tree for itself (the same numbers, so the same walk)
 // and sums its part of the rows; the totals meet in shared memory across
-// the cluster, and the CTA in whose part the goal lies finds the token.
+// the cluster, and the warp in whose part the goal lies finds the token.
+//
+// Measured on the device (chains of 8 nodes, f32 with q, 131,072 elements):
+// 64 trees 16.0 us, the 67 MB of their last rows at 4.2 TB/s (0.62 of a
+// copy's rate).  By time stamps 2 us go to the nodes and their elements, 0.5 to 3
+// to the walk, 8 to 9 to the rows, 1 to the totals and 1.3 to the search.  One
+// tree over 32,768 elements: 4.8 us.
 #include <stdint.h>
 
 #include "common.cuh"
@@ -39,8 +45,8 @@ constexpr int kUBits = 24;
 __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 
 // Sums of fix(x) = floor(2^40 x) for 0 <= x < 4.  A conversion to 64-bit whole
-// numbers runs at the FP64 pipe's rate (it took two thirds of the call), so x
-// is taken apart by float operations, all of them exact: added to 2^23 and
+// numbers runs at the FP64 pipe's rate (with it 64 trees took 27 us instead of
+// 18, that pipe two thirds of the time), so x is taken apart by float operations, all of them exact: added to 2^23 and
 // rounded towards zero, a number below 2^23 leaves its whole part in the
 // low bits of the sum.  floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x)
 // and lo the same of what is left of it.
@@ -70,7 +76,8 @@ __device__ __forceinline__ float mass_of(long long sum) {
 }
 
 // w / mass for a residual's w >= 0.  Half of a residual is zeros, and a
-// zero would take the division's slow path.
+// zero would take the division's slow path (16 trees of 32 nodes, up to three
+// siblings drawn from q, 50,001 elements: 32 us, 17 without it).
 __device__ __forceinline__ float divided(float w, float mass) {
     const float x = __fdiv_rn(w > 0.f ? w : mass, mass);
     return w > 0.f ? x : 0.f;
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, KEEP ? 1 : 2)
     bool ok = true;
     long long before = 0;  // mass of the CTAs before this one
     // Total mass of the node's rows after n refusals.  Each CTA's goes to all
-    // others; round r's barrier and totals are used again in round r + 2, which
+    // others by a store that counts on their barriers (a cluster barrier took 1.5 us); round r's barrier and totals are used again in round r + 2, which
     // no CTA enters before every other one has left round r.
     auto total_mass = [&](int n) -> long long {
         const long long mine = mass(n);

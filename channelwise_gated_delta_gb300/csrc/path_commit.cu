@@ -7,10 +7,15 @@
 //     s_ij <- s_ij + k_i d_j
 // The columns j of a state never meet, so the state is cut along them and
 // stays in registers over the whole path: read once, written once, which is
-// what bounds the call for paths of up to about ten nodes (three operations an element
-// and node against eight bytes an element).
+// what bounds the call for paths of up to about ten nodes (three operations
+// an element and node against eight bytes an element).
 //
-// A warp owns 16 columns of a head's state: lane (cq = lane % 4, rg = lane /
+// Measured on the device: 64 x 32 heads of 128 x 128, paths of 1 to 8 nodes,
+// 50.2 us (277 MB at 5.5 TB/s, 0.81 of a copy's rate), of one node 45.7 us (0.86), of 64
+// nodes 283 us (0.29 us a head and node on an SM, bound by its FMA pipes); 64 x
+// 32 heads of 64 x 64, paths of 1 to 5 nodes, 17.7 us (4.0 TB/s).
+//
+// The kernel for heads other than 128 x 128: a warp owns 16 columns of a head's state: lane (cq = lane % 4, rg = lane /
 // 4) holds columns 4 cq .. 4 cq + 3 of the rows rg + 8 m.  A row's 16 columns
 // are 64 contiguous bytes, the sum over the rows stays inside the warp, and
 // between the nodes no warp waits for another.  The arithmetic is on pairs of
@@ -60,8 +65,9 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
 }
 
 // One CTA: kCols columns of one head, two warps.  (Four warps, which stage k
-// and exp(g) half as often: 2 x 32 heads of 64 x 64, paths of up to 6 nodes, 3.3 us either way; 64 x 32
-// heads 18.3 against 18.6, of 128 x 64 31.4 against 31.5.)
+// and exp(g) half as often: 2 x 32 heads of 64 x 64, paths of up to 6 nodes,
+// 3.3 us either way; 64 x 32 heads 18.3 against 18.6, of 128 x 64 31.4
+// against 31.5.)
 template <typename Tin, int DK, bool GS>
 __global__ void __launch_bounds__(2 * kCols, DK == 128 ? 6 : 8)
     gdr_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v,
@@ -191,16 +197,25 @@ __global__ void __launch_bounds__(2 * kCols, DK == 128 ? 6 : 8)
 // One CTA per SM walks heads blockIdx.x, + gridDim.x, ...  The kernel above
 // waits for a chain of loads (path length, path, k / g / v of its nodes)
 // before a head's first step and has nothing else to do meanwhile.  Here a
-// head belongs to one of two groups of four warps in turn; a producer warp
-// per group brings its heads' nodes (k, exp(g), v, beta as float32, four
-// nodes a slot, the next four's loads in flight) and states (three 64 KB
-// buffers, which the groups share in the order of the heads).  A group copies
-// its state into registers, frees the buffer at once and stores from the
-// registers, so that all three buffers are reads ahead.
+// head belongs to one of two groups of four warps in turn; two producer warps
+// per group bring its heads' nodes (k, exp(g), v, beta as float32, two nodes
+// each of a slot of four, the next slot's loads in flight), the first of them
+// also the states (three 64 KB buffers, which the groups share in the order
+// of the heads).  A group copies its state into registers, frees the buffer
+// at once and stores from the registers, so that all three buffers are
+// reads ahead.
 //
 // Warp w of a group owns columns 32 w .. + 31: lane (cq = lane % 8, rg = lane
 // / 8) holds columns 4 cq .. + 3 of the rows 4 rg + 16 m .. + 3 (m < 8) as
 // pairs of rows, so that k and a are pairs as they lie in shared memory.
+//
+// Against the kernel above at 128 x 128 (32 heads / 64 x 32 heads, all paths of
+// one length): one node 4.2 / 45.7 us against 3.9 / 46.7, 8 nodes 7.2 / 55
+// against 8.8 / 73, 64 nodes 29 / 283 against 60 / 443.  One producer warp per
+// group instead of two: 67 us for 64 x 32 heads with paths of 1 to 8 nodes,
+// against 50.  Taking four nodes in one step, with the decays multiplied out, saves a
+// quarter of the operations and costs the producers more: 261 us for 64
+// nodes, but 5.2 / 47.4 for one and 54 for 1 to 8.
 constexpr int kD = 128;
 constexpr int kBufs = 3;
 constexpr int kSlots = 2;
