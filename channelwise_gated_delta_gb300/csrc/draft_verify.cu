@@ -46,9 +46,9 @@ __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 
 // Sums of fix(x) = floor(2^40 x) for 0 <= x < 4.  A conversion to 64-bit whole
 // numbers runs at the FP64 pipe's rate (with it 64 trees took 27 us instead of
-// 18, that pipe two thirds of the time), so x is taken apart by float operations, all of them exact: added to 2^23 and
-// rounded towards zero, a number below 2^23 leaves its whole part in the
-// low bits of the sum.  floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x)
+// 18, that pipe two thirds of the time), so x is taken apart by float
+// operations, all of them exact: added to 2^23 and rounded towards zero, a
+// number below 2^23 leaves its whole part in the low bits of the sum.  floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x)
 // and lo the same of what is left of it.
 struct Mass {
     uint32_t hi = 0, lo = 0;  // of at most 64 elements: a warp's sums fit 32 bits
@@ -199,15 +199,18 @@ __global__ void __launch_bounds__(THREADS, KEEP ? 1 : 2)
     __shared__ float s_coin[kMaxNodes], s_p[kMaxNodes], s_q[kMaxNodes];
     __shared__ float s_norm[kMaxNodes];   // with q: the mass of each residual
     __shared__ int s_refused[kMaxNodes];  // without q: the nodes refused
-    __shared__ long long s_warp[kWarps], s_before[kWarps];  // a warp's mass, that of those before it
+    __shared__ long long s_warp[kWarps], s_before[kWarps];  // a warp's mass, those before it
     __shared__ long long s_total[2][kMaxCluster];
     __shared__ uint64_t s_bar[2];
     __shared__ int s_here, s_out, s_more, s_summed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x >> log_cluster, cluster = 1 << log_cluster;
     const int rank = blockIdx.x - (b << log_cluster);
-    if (tid < 2) sm100::mbar_init(&s_bar[tid], 1);
-    if (tid == 0) sm100::fence_mbar_init();
+    if (tid == 0) {
+        sm100::mbar_init(&s_bar[0], 1);
+        sm100::mbar_init(&s_bar[1], 1);
+        sm100::fence_mbar_init();
+    }
     __syncwarp();
     cluster_arrive();  // (1) this CTA runs and its barriers are there: others may write to it
 
@@ -379,8 +382,9 @@ __global__ void __launch_bounds__(THREADS, KEEP ? 1 : 2)
     bool ok = true;
     long long before = 0;  // mass of the CTAs before this one
     // Total mass of the node's rows after n refusals.  Each CTA's goes to all
-    // others by a store that counts on their barriers (a cluster barrier took 1.5 us); round r's barrier and totals are used again in round r + 2, which
-    // no CTA enters before every other one has left round r.
+    // others by a store that counts on their barriers (a cluster barrier took
+    // 1.5 us); round r's barrier and totals are used again in round r + 2,
+    // which no CTA enters before every other one has left round r.
     auto total_mass = [&](int n) -> long long {
         const long long mine = mass(n);
         if (lane == 0) s_warp[warp] = mine;
@@ -538,7 +542,8 @@ __global__ void __launch_bounds__(THREADS, KEEP ? 1 : 2)
     const float top = 1.f - 1.f / (1 << kUBits);
     const long long m = (long long)__fmul_rn(fminf(fmaxf(uu, 0.f), top), (float)(1 << kUBits));
     const long long low = (1 << kUBits) - 1;
-    long long goal = (total >> kUBits) * m + (((total & low) * m) >> kUBits);  // floor(total m / 2^24)
+    // floor(total m / 2^24)
+    long long goal = (total >> kUBits) * m + (((total & low) * m) >> kUBits);
     goal -= before + s_before[warp];
     if (goal < 0 || goal >= s_warp[warp]) return;  // in another warp's part
     // the group of batches, the batch, the unit, the lane, the element
@@ -729,8 +734,8 @@ extern "C" GDR_API gdr_status gdr_verify_drafts(const void *p, const void *q, co
     for (int o = 6; o < 9; ++o)  // an output against the inputs and the outputs before it
         if (overlaps_any(args[o], args, o)) return GDR_ERR_ALIAS;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const VerifyArgs a{p,   q,   tokens,    parent,    coins,   u, path, n_path, next_token, B, T, V,
-                       ldp, ldq, parent_sb, parent_st, max_path};
+    const VerifyArgs a{p, q, tokens, parent, coins, u, path, n_path, next_token,
+                       B, T, V, ldp, ldq, parent_sb, parent_st, max_path};
     const cudaError_t e =
         prob_dtype == GDR_BF16
             ? (q ? launch_q<__nv_bfloat16, true>(a, s) : launch_q<__nv_bfloat16, false>(a, s))

@@ -15,12 +15,13 @@
 // nodes 283 us (0.29 us a head and node on an SM, bound by its FMA pipes); 64 x
 // 32 heads of 64 x 64, paths of 1 to 5 nodes, 17.7 us (4.0 TB/s).
 //
-// The kernel for heads other than 128 x 128: a warp owns 16 columns of a head's state: lane (cq = lane % 4, rg = lane /
-// 4) holds columns 4 cq .. 4 cq + 3 of the rows rg + 8 m.  A row's 16 columns
-// are 64 contiguous bytes, the sum over the rows stays inside the warp, and
-// between the nodes no warp waits for another.  The arithmetic is on pairs of
-// columns (fma.rn.f32x2: two roundings as by two fma).  k and exp(g) of a
-// batch of nodes are staged in shared memory as (k, k, a, a), the pairs' form.
+// The kernel for heads other than 128 x 128: a warp owns 16 columns of a head's
+// state; lane (cq = lane % 4, rg = lane / 4) holds columns 4 cq .. 4 cq + 3 of
+// the rows rg + 8 m.  A row's 16 columns are 64 contiguous bytes, the sum over
+// the rows stays inside the warp, and between the nodes no warp waits for
+// another.  The arithmetic is on pairs of columns (fma.rn.f32x2: two roundings
+// as by two fma).  k and exp(g) of a batch of nodes are staged in shared memory
+// as (k, k, a, a), the pairs' form.
 #include <stdint.h>
 
 #include "common.cuh"
@@ -159,7 +160,8 @@ __global__ void __launch_bounds__(2 * kCols, DK == 128 ? 6 : 8)
                     acc[m & 1][h] = m < 2 ? mul2(kk, s[m][h]) : fma2(kk, s[m][h], acc[m & 1][h]);
                 }
             }
-            const float2 x = split(add2(acc[0][0], acc[1][0])), y = split(add2(acc[0][1], acc[1][1]));
+            const float2 x = split(add2(acc[0][0], acc[1][0]));
+            const float2 y = split(add2(acc[0][1], acc[1][1]));
             // over the eight row groups: halving the columns twice, then one
             // sum left per lane, that of column 4 cq + 2 (rg & 1) + (rg >> 1 & 1)
             const bool odd = rg & 1, high = rg & 2;
@@ -172,7 +174,8 @@ __global__ void __launch_bounds__(2 * kCols, DK == 128 ? 6 : 8)
             const int mine = 4 * cq + (odd ? 2 : 0) + (high ? 1 : 0);
             const float b_t = __shfl_sync(0xffffffffu, b_batch, c);
             const float d = b_t * (s_v[c][warp * kWarpCols + mine] - sum);
-            const Pair d0 = pair(__shfl_sync(0xffffffffu, d, cq), __shfl_sync(0xffffffffu, d, cq + 8));
+            const Pair d0 =
+                pair(__shfl_sync(0xffffffffu, d, cq), __shfl_sync(0xffffffffu, d, cq + 8));
             const Pair d1 =
                 pair(__shfl_sync(0xffffffffu, d, cq + 4), __shfl_sync(0xffffffffu, d, cq + 12));
 #pragma unroll
@@ -327,7 +330,8 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
         // Two warps per group: nodes 2 half, 2 half + 1 of each slot; the
         // first also asks for the states and writes the slot's count.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        const int grp = (warp - kGroups * kGroupWarps) & 1, half = (warp - kGroups * kGroupWarps) >> 1;
+        const int producer = warp - kGroups * kGroupWarps;
+        const int grp = producer & 1, half = producer >> 1;
         int next_state = grp;  // the group's next head whose state has not been asked for
         // Asks for the states of heads up to `upto`, waiting for their buffers,
         // and up to `may` where that needs no wait.  A buffer's barriers tell
@@ -474,7 +478,8 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
             if (lane == 0) atomicOr(dev_error, 1);
             // never leave with loads in flight into this CTA: the last
             // states asked for, one per buffer at most
-            for (int i = next_state - kGroups, j = 0; half == 0 && h0 && i >= 0 && j < kBufs; i -= kGroups, ++j)
+            for (int i = next_state - kGroups, j = 0; half == 0 && h0 && i >= 0 && j < kBufs;
+                 i -= kGroups, ++j)
                 sm100::mbar_wait_bounded(&sh.state_full[i % kBufs], (uint32_t)(i / kBufs) & 1u,
                                          kWaitNs);
         }
@@ -535,7 +540,8 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
                 ulonglong2 keys[8];
 #pragma unroll
                 for (int m = 0; m < 8; ++m) {
-                    const ulonglong2 kk = keys[m] = *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
+                    const ulonglong2 kk = keys[m] =
+                        *reinterpret_cast<const ulonglong2 *>(kr + 16 * m);
                     const ulonglong2 aa = *reinterpret_cast<const ulonglong2 *>(ar + 16 * m);
 #pragma unroll
                     for (int r = 0; r < 2; ++r)

@@ -21,9 +21,9 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from channelwise_gated_delta_gb300 import (gdr_commit_path, gdr_forward, gdr_forward_tree,  # noqa: E402
-                                           gdr_state_cache, gdr_state_load, gdr_state_store,
-                                           gdr_verify_drafts)
+from channelwise_gated_delta_gb300 import (gdr_commit_path, gdr_forward,  # noqa: E402
+                                           gdr_forward_tree, gdr_state_cache, gdr_state_load,
+                                           gdr_state_store, gdr_verify_drafts)
 from channelwise_gated_delta_gb300.inputs import draw_parents  # noqa: E402
 
 
@@ -65,7 +65,8 @@ def draft_tree(toy, root, parent, gen):
     return tokens, toy.draft(tokens)
 
 
-def run(batch=4, steps=8, T=12, branching=2, max_path=4, V=512, layers=2, HK=2, HV=4, d=128, seed=1):
+def run(batch=4, steps=8, T=12, branching=2, max_path=4, V=512, layers=2, HK=2, HV=4, d=128,
+        seed=1):
     toy = Toy(V, layers, HK, HV, d)
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)

@@ -101,8 +101,8 @@ def test_batches(B):
 def test_refusal_of_everything():
     d = problem(4, 40, 300, "star", True, seed=7)
     d["coins"].fill_(1.0 - 2.0 ** -24)
-    d["q"] = torch.softmax(3.0 * torch.randn(4, 40, 300, generator=torch.Generator().manual_seed(1)),
-                           -1)
+    gen = torch.Generator().manual_seed(1)
+    d["q"] = torch.softmax(3.0 * torch.randn(4, 40, 300, generator=gen), -1)
     d["tokens"][:] = d["q"][:, 0].argmax(-1)[:, None].to(torch.int32)
     check(d)
     d["q"] = None   # the same token proposed again and again: refused once, then without mass
@@ -130,7 +130,8 @@ def test_rows_without_mass_and_strange_values():
         check(d)
 
 
-@pytest.mark.parametrize("u", [0.0, 2.0 ** -24, 0.5, 1.0 - 2.0 ** -24, 1.0, 7.0, -1.0, float("nan")])
+@pytest.mark.parametrize("u", [0.0, 2.0 ** -24, 0.5, 1.0 - 2.0 ** -24, 1.0, 7.0, -1.0,
+                               float("nan")])
 def test_random_numbers_at_their_ends(u):
     d = problem(3, 3, 1030, "chain", True, seed=9)
     d["u"].fill_(u)
