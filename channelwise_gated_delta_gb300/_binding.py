@@ -412,7 +412,8 @@ def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=N
     if max_path is None:
         max_path = T if path is None else path.shape[-1]
     if path is None:
-        path = torch.empty_strided((B, max_path), (max_path, 1), dtype=i32, device=p.device)
+        path = (torch.empty_like(tokens) if max_path == T else
+                torch.empty_strided((B, max_path), (max_path, 1), dtype=i32, device=p.device))
     else:
         _given("path", path, (B, max_path), i32, index)
     if n_path is None:
