@@ -200,10 +200,10 @@ __global__ void __launch_bounds__(2 * kCols, DK == 128 ? 6 : 8)
 // One CTA per SM walks heads blockIdx.x, + gridDim.x, ...  The kernel above
 // waits for a chain of loads (path length, path, k / g / v of its nodes)
 // before a head's first step and has nothing else to do meanwhile.  Here a
-// head belongs to one of two groups of four warps in turn; two producer warps
-// per group bring its heads' nodes (k, exp(g), v, beta as float32, two nodes
-// each of a slot of four, the next slot's loads in flight), the first of them
-// also the states (three 64 KB buffers, which the groups share in the order
+// head belongs to one of two groups of four warps in turn; two or four producer
+// warps per group bring its heads' nodes (k, exp(g), v, beta as float32, one or
+// two nodes each of a slot of four, the next slot's loads in flight), the first
+// of them also the states (three 64 KB buffers, which the groups share in the order
 // of the heads).  A group copies its state into registers, frees the buffer
 // at once and stores from the registers, so that all three buffers are
 // reads ahead.
@@ -225,12 +225,20 @@ constexpr int kSlots = 2;
 constexpr int kSlotNodes = 4;
 constexpr int kGroups = 2;
 constexpr int kGroupWarps = 4;
-constexpr int kHalf = kSlotNodes / 2;  // nodes of a slot per producer warp
-// Two warpgroups of states and one of producers: registers move between
-// warpgroups.  384 threads are launched with 168 registers each, 64512 in
-// all: 2 x 128 x 200 + 128 x 104.
-constexpr int kBulkThreads = (kGroups + 1) * kGroupWarps * 32;
-constexpr int kStateRegs = 208, kProducerRegs = 88;
+// Producer warps per group, and the registers of a thread: the warpgroups of
+// the states are given some that the producers' were launched with.  float32
+// nodes are twice the bytes and want twice the warps (64 x 32 heads, paths of 1
+// to 8 nodes: 51 us, 58 with two; bf16: 50 and 50, at 1 to 20 nodes 82 and 75).
+template <typename Tin>
+struct Producers {  // 384 threads of 168 registers: 2 x 128 x 208 + 128 x 88
+    static constexpr int kWarps = 2, kStateRegs = 208, kRegs = 88;
+};
+template <>
+struct Producers<float> {  // 512 threads of 128 registers: 2 x 128 x 184 + 2 x 128 x 72
+    static constexpr int kWarps = 4, kStateRegs = 184, kRegs = 72;
+};
+template <typename Tin>
+constexpr int kBulkThreads = kGroups * (kGroupWarps + Producers<Tin>::kWarps) * 32;
 constexpr uint32_t kStateBytes = kD * kD * 4;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 
@@ -299,12 +307,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 }
 
 template <typename Tin, bool GS>
-__global__ void __launch_bounds__(kBulkThreads, 1)
+__global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
     gdr_commit_bulk_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v,
                            const float *__restrict__ g, const float *__restrict__ beta,
                            const float *h0, float *ht, const int *__restrict__ path,
                            const int *__restrict__ n_path, int T, int HK, int HV, int max_path,
                            int nheads, int *dev_error) {
+    constexpr int kProducers = Producers<Tin>::kWarps;
+    constexpr int kHalf = kSlotNodes / kProducers;  // nodes of a slot per producer warp
     extern __shared__ __align__(128) unsigned char smem_raw[];
     BulkShared &sh = *reinterpret_cast<BulkShared *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -315,7 +325,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
         }
         for (int i = 0; i < kGroups; ++i)
             for (int j = 0; j < kSlots; ++j) {
-                sm100::mbar_init(&sh.full[i][j], kSlotNodes / kHalf);
+                sm100::mbar_init(&sh.full[i][j], kProducers);
                 sm100::mbar_init(&sh.empty[i][j], kGroupWarps);
             }
         sm100::fence_mbar_init();
@@ -326,12 +336,12 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
     bool ok = true;
 
     if (warp >= kGroups * kGroupWarps) {
-        // ---- producer of group grp: heads grp, grp + 2, ...
-        // Two warps per group: nodes 2 half, 2 half + 1 of each slot; the
-        // first also asks for the states and writes the slot's count.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        // ---- producers of group grp: heads grp, grp + 2, ...
+        // Warp number `half` brings kHalf nodes of each slot; the first also
+        // asks for the states and writes the slot's count.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Producers<Tin>::kRegs));
         const int producer = warp - kGroups * kGroupWarps;
-        const int grp = producer & 1, half = producer >> 1;
+        const int grp = producer / kProducers, half = producer % kProducers;
         int next_state = grp;  // the group's next head whose state has not been asked for
         // Asks for the states of heads up to `upto`, waiting for their buffers,
         // and up to `may` where that needs no wait.  A buffer's barriers tell
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1)
     }
 
     // ---- group grp
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Producers<Tin>::kStateRegs));
     const int grp = warp / kGroupWarps, cq = lane & 7, rg = lane >> 3;
     const int col = 32 * (warp % kGroupWarps) + 4 * cq;
     const bool odd = rg & 1, high = rg & 2;
@@ -618,11 +628,20 @@ cudaError_t launch_bulk(const CommitArgs &a, cudaStream_t stream) {
     const int nheads = a.B * a.HV;  // at most 2^30
     const int grid = nheads < sms ? nheads : sms;
     const auto kernel = gdr_commit_bulk_kernel<Tin, GS>;
+    // The groups wait for registers that the block has to have been launched with.
+    static const int launched = [kernel] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+    }();
+    using P = Producers<Tin>;
+    constexpr int kWanted =
+        kGroups * 32 * (kGroupWarps * P::kStateRegs + P::kWarps * P::kRegs);
+    if (launched * kBulkThreads<Tin> < kWanted) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(BulkShared));
     if (e != cudaSuccess) return e;
     trace_begin(kKernCommit, stream);
-    kernel<<<grid, kBulkThreads, sizeof(BulkShared), stream>>>(
+    kernel<<<grid, kBulkThreads<Tin>, sizeof(BulkShared), stream>>>(
         static_cast<const Tin *>(a.k), static_cast<const Tin *>(a.v), a.g, a.beta, a.h0, a.ht,
         a.path, a.n_path, a.T, a.HK, a.HV, a.max_path, nheads, err);
     trace_end(kKernCommit, stream);
