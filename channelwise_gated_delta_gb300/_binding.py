@@ -5,7 +5,14 @@ contiguity, their data pointers and the current CUDA stream are handed to the
 library, and a non-OK status becomes an exception.  Every step of the forward
 pass runs in the library's CUDA kernels; there is no fallback of any kind, and
 the first call raises if the library has not been built.
+
+Streams: a call is enqueued on ``stream``, torch's current one by default.  On a
+given stream the caller orders the inputs (and given outputs) against the work on
+other streams and keeps them alive until the stream has passed the call, as for
+every use of a tensor on a stream not its own; outputs and workspaces that the call
+allocates are memory of that stream.
 """
+import contextlib
 import ctypes
 import os
 
@@ -127,6 +134,16 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_CURRENT_MEMORY = contextlib.nullcontext()
+
+
+def _memory_of(stream):
+    """Where a call on ``stream`` allocates: among that stream's blocks.  A block of the current
+    stream may have work on it queued there, which a kernel on another stream would not wait
+    for, and would be handed out there again as soon as it is dropped."""
+    return _CURRENT_MEMORY if stream is None else torch.cuda.stream(stream)
+
+
 def _dtype_code(dt, what="q/k/v"):
     if dt == torch.bfloat16:
         return GDR_BF16
@@ -176,15 +193,18 @@ def gdr_forward(q, k, v, g, beta, h0=None, out=None, ht=None, chunk=64, stream=N
         raise TypeError("g and beta must be float32")
     if h0 is not None and (tuple(h0.shape) != (B, HV, dk, dv) or h0.dtype != torch.float32):
         raise ValueError("h0 must be float32 [B, HV, dk, dv]")
+    need = int(lib.gdr_workspace_bytes(B, T, HK, HV, dk, dv, chunk, code, flags))
     if out is None:
-        out = torch.empty(B, T, HV, dv, dtype=q.dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(B, T, HV, dv, dtype=q.dtype, device=dev)
     if ht is None and store_ht:
-        ht = torch.empty(B, HV, dk, dv, dtype=torch.float32, device=dev)
+        with _memory_of(stream):
+            ht = torch.empty(B, HV, dk, dv, dtype=torch.float32, device=dev)
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        with _memory_of(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    need = int(lib.gdr_workspace_bytes(B, T, HK, HV, dk, dv, chunk, code, flags))
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_ptr = _ptr(workspace) if need > 0 else None
     ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
     st = lib.gdr_forward_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out),
@@ -276,17 +296,20 @@ def gdr_forward_varlen(q, k, v, g, beta, cu_seqlens, h0=None, out=None, ht=None,
         raise TypeError("g and beta must be float32")
     if h0 is not None and (tuple(h0.shape) != (n, HV, dk, dv) or h0.dtype != torch.float32):
         raise ValueError("h0 must be float32 [N, HV, dk, dv]")
+    need = int(lib.gdr_varlen_workspace_bytes(cu, n, HK, HV, dk, dv, chunk, code, flags))
     if out is None:
-        out = torch.empty(total, HV, dv, dtype=q.dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(total, HV, dv, dtype=q.dtype, device=dev)
     elif out.dim() == 4:
         out = out[0]
     if ht is None and store_ht:
-        ht = torch.empty(n, HV, dk, dv, dtype=torch.float32, device=dev)
+        with _memory_of(stream):
+            ht = torch.empty(n, HV, dk, dv, dtype=torch.float32, device=dev)
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        with _memory_of(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    need = int(lib.gdr_varlen_workspace_bytes(cu, n, HK, HV, dk, dv, chunk, code, flags))
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_ptr = _ptr(workspace) if need > 0 else None
     ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
     st = lib.gdr_forward_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
@@ -336,13 +359,15 @@ def gdr_forward_tree(q, k, v, g, beta, parent, h0=None, out=None, stream=None, w
     if tuple(par.shape) != (B, T):
         raise ValueError("parent must be [B, T]")
     par_c = par.numpy().ctypes.data_as(ctypes.POINTER(ctypes.c_int))
+    need = int(lib.gdr_tree_workspace_bytes(B, T, HK, HV, dk, dv, code, flags))
     if out is None:
-        out = torch.empty(B, T, HV, dv, dtype=q.dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(B, T, HV, dv, dtype=q.dtype, device=dev)
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        with _memory_of(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    need = int(lib.gdr_tree_workspace_bytes(B, T, HK, HV, dk, dv, code, flags))
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_ptr = _ptr(workspace) if need > 0 else None
     ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
     st = lib.gdr_forward_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out),
@@ -411,19 +436,20 @@ def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=N
         ldq, q_ptr = _prob_rows("q", q), q.data_ptr()
     if max_path is None:
         max_path = T if path is None else path.shape[-1]
-    if path is None:
-        path = (torch.empty_like(tokens) if max_path == T else
-                torch.empty_strided((B, max_path), (max_path, 1), dtype=i32, device=p.device))
-    else:
-        _given("path", path, (B, max_path), i32, index)
-    if n_path is None:
-        n_path = torch.empty_like(u, dtype=i32)
-    else:
-        _given("n_path", n_path, (B,), i32, index)
-    if next_token is None:
-        next_token = torch.empty_like(u, dtype=i32)
-    else:
-        _given("next_token", next_token, (B,), i32, index)
+    with _memory_of(stream):
+        if path is None:
+            path = (torch.empty_like(tokens) if max_path == T else
+                    torch.empty_strided((B, max_path), (max_path, 1), dtype=i32, device=p.device))
+        else:
+            _given("path", path, (B, max_path), i32, index)
+        if n_path is None:
+            n_path = torch.empty_like(u, dtype=i32)
+        else:
+            _given("n_path", n_path, (B,), i32, index)
+        if next_token is None:
+            next_token = torch.empty_like(u, dtype=i32)
+        else:
+            _given("next_token", next_token, (B,), i32, index)
     st = lib.gdr_verify_drafts(p.data_ptr(), q_ptr, tokens.data_ptr(), parent.data_ptr(),
                                coins.data_ptr(), u.data_ptr(), path.data_ptr(),
                                n_path.data_ptr(), next_token.data_ptr(), B, T, V,
@@ -464,7 +490,8 @@ def gdr_commit_path(k, v, g, beta, path, n_path, h0=None, ht=None, stream=None, 
         _given("h0", h0, (B, HV, dk, dv), f32, index)
         h0_ptr = h0.data_ptr()
     if ht is None:
-        ht = torch.empty((B, HV, dk, dv), dtype=f32, device=k.device)
+        with _memory_of(stream):
+            ht = torch.empty((B, HV, dk, dv), dtype=f32, device=k.device)
     elif ht is not h0:
         _given("ht", ht, (B, HV, dk, dv), f32, index)
     st = lib.gdr_commit_path(k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), h0_ptr,
@@ -512,7 +539,8 @@ def gdr_state_load(cache, scale, slots, out=None, stream=None):
     lib = load_library()
     N, n_slots, HV, dk, dv, index = _state_cache_sizes(slots, cache, scale)
     if out is None:
-        out = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=cache.device)
+        with _memory_of(stream):
+            out = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=cache.device)
     else:
         _given("out", out, (N, HV, dk, dv), torch.float32, index)
     st = lib.gdr_state_load(cache.data_ptr(), scale.data_ptr(), slots.data_ptr(), out.data_ptr(),
@@ -558,11 +586,12 @@ def gdr_forward_host(q, k, v, g, beta, h0, out, ht, chunk=64, stream=None, stagi
         if t is not None and (tuple(t.shape) != (B, HV, dk, dv) or t.dtype != torch.float32):
             raise ValueError("%s must be float32 [B, HV, dk, dv]" % name)
     dev = torch.device("cuda") if device is None else torch.device(device)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     need = int(lib.gdr_host_staging_bytes(B, T, HK, HV, dk, dv, chunk, code))
     if need > 0 and (staging is None or staging.numel() * staging.element_size() < need):
-        staging = torch.empty(need, dtype=torch.uint8, device=dev)
+        with _memory_of(stream):
+            staging = torch.empty(need, dtype=torch.uint8, device=dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
     st_ptr = _ptr(staging) if need > 0 else None
     st_bytes = staging.numel() * staging.element_size() if need > 0 else 0
     st = lib.gdr_forward_host(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
