@@ -134,6 +134,27 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _on(index, entry):
+    """``entry`` as called with device ``index`` current: the library looks up SMs, its error word
+    and the target of its launches on the current device."""
+    if torch._C._cuda_getDevice() == index:  # the usual case costs one comparison
+        return entry
+
+    def there(*args):
+        with torch.cuda.device(index):
+            return entry(*args)
+    return there
+
+
+def _stream_of(stream, index):
+    """The address of a CUDA stream of device ``index``; that of its current one for None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError("stream must be one of cuda:%d, got one of %s" % (index, stream.device))
+    return stream.cuda_stream
+
+
 _CURRENT_MEMORY = contextlib.nullcontext()
 
 
@@ -193,7 +214,7 @@ def gdr_forward(q, k, v, g, beta, h0=None, out=None, ht=None, chunk=64, stream=N
         raise TypeError("g and beta must be float32")
     if h0 is not None and (tuple(h0.shape) != (B, HV, dk, dv) or h0.dtype != torch.float32):
         raise ValueError("h0 must be float32 [B, HV, dk, dv]")
-    need = int(lib.gdr_workspace_bytes(B, T, HK, HV, dk, dv, chunk, code, flags))
+    need = int(_on(dev.index, lib.gdr_workspace_bytes)(B, T, HK, HV, dk, dv, chunk, code, flags))
     if out is None:
         with _memory_of(stream):
             out = torch.empty(B, T, HV, dv, dtype=q.dtype, device=dev)
@@ -203,13 +224,12 @@ def gdr_forward(q, k, v, g, beta, h0=None, out=None, ht=None, chunk=64, stream=N
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         with _memory_of(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     ws_ptr = _ptr(workspace) if need > 0 else None
     ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
-    st = lib.gdr_forward_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out),
-                            _ptr(ht), B, T, HK, HV, dk, dv, chunk,
-                            ctypes.c_void_p(stream.cuda_stream), code, ws_ptr, ws_bytes, flags)
+    st = _on(dev.index, lib.gdr_forward_ex)(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out), _ptr(ht), B, T, HK,
+        HV, dk, dv, chunk,
+        ctypes.c_void_p(_stream_of(stream, dev.index)), code, ws_ptr, ws_bytes, flags)
     _check(lib, st)
     return out, ht
 
@@ -296,7 +316,8 @@ def gdr_forward_varlen(q, k, v, g, beta, cu_seqlens, h0=None, out=None, ht=None,
         raise TypeError("g and beta must be float32")
     if h0 is not None and (tuple(h0.shape) != (n, HV, dk, dv) or h0.dtype != torch.float32):
         raise ValueError("h0 must be float32 [N, HV, dk, dv]")
-    need = int(lib.gdr_varlen_workspace_bytes(cu, n, HK, HV, dk, dv, chunk, code, flags))
+    need = int(_on(dev.index, lib.gdr_varlen_workspace_bytes)(cu, n, HK, HV, dk, dv, chunk, code,
+                   flags))
     if out is None:
         with _memory_of(stream):
             out = torch.empty(total, HV, dv, dtype=q.dtype, device=dev)
@@ -308,13 +329,12 @@ def gdr_forward_varlen(q, k, v, g, beta, cu_seqlens, h0=None, out=None, ht=None,
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         with _memory_of(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     ws_ptr = _ptr(workspace) if need > 0 else None
     ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
-    st = lib.gdr_forward_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
-                                _ptr(out), _ptr(ht), cu, n, HK, HV, dk, dv, chunk,
-                                ctypes.c_void_p(stream.cuda_stream), code, ws_ptr, ws_bytes, flags)
+    st = _on(dev.index, lib.gdr_forward_varlen)(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out), _ptr(ht), cu, n, HK,
+        HV, dk, dv, chunk,
+        ctypes.c_void_p(_stream_of(stream, dev.index)), code, ws_ptr, ws_bytes, flags)
     _check(lib, st)
     return (out.unsqueeze(0) if lead else out), ht
 
@@ -359,20 +379,18 @@ def gdr_forward_tree(q, k, v, g, beta, parent, h0=None, out=None, stream=None, w
     if tuple(par.shape) != (B, T):
         raise ValueError("parent must be [B, T]")
     par_c = par.numpy().ctypes.data_as(ctypes.POINTER(ctypes.c_int))
-    need = int(lib.gdr_tree_workspace_bytes(B, T, HK, HV, dk, dv, code, flags))
+    need = int(_on(dev.index, lib.gdr_tree_workspace_bytes)(B, T, HK, HV, dk, dv, code, flags))
     if out is None:
         with _memory_of(stream):
             out = torch.empty(B, T, HV, dv, dtype=q.dtype, device=dev)
     if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
         with _memory_of(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     ws_ptr = _ptr(workspace) if need > 0 else None
     ws_bytes = workspace.numel() * workspace.element_size() if need > 0 else 0
-    st = lib.gdr_forward_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out),
-                              par_c, B, T, HK, HV, dk, dv, ctypes.c_void_p(stream.cuda_stream), code,
-                              ws_ptr, ws_bytes, flags)
+    st = _on(dev.index, lib.gdr_forward_tree)(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out), par_c, B, T, HK, HV,
+        dk, dv, ctypes.c_void_p(_stream_of(stream, dev.index)), code, ws_ptr, ws_bytes, flags)
     _check(lib, st)
     return out
 
@@ -387,11 +405,6 @@ def _given(name, t, shape, dtype, index):
                          % (name, dtype, list(shape), t.dtype, list(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-
-
-def _stream_of(stream, index):
-    """The CUDA stream's address; the current one of device ``index`` for None."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _prob_rows(name, t):
@@ -450,11 +463,10 @@ def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=N
             next_token = torch.empty_like(u, dtype=i32)
         else:
             _given("next_token", next_token, (B,), i32, index)
-    st = lib.gdr_verify_drafts(p.data_ptr(), q_ptr, tokens.data_ptr(), parent.data_ptr(),
-                               coins.data_ptr(), u.data_ptr(), path.data_ptr(),
-                               n_path.data_ptr(), next_token.data_ptr(), B, T, V,
-                               _prob_rows("p", p), ldq, parent.stride(0), parent.stride(1),
-                               max_path, _stream_of(stream, index), code)
+    st = _on(index, lib.gdr_verify_drafts)(
+        p.data_ptr(), q_ptr, tokens.data_ptr(), parent.data_ptr(), coins.data_ptr(), u.data_ptr(),
+        path.data_ptr(), n_path.data_ptr(), next_token.data_ptr(), B, T, V, _prob_rows("p", p),
+        ldq, parent.stride(0), parent.stride(1), max_path, _stream_of(stream, index), code)
     if st != GDR_OK:
         _check(lib, st)
     return path, n_path, next_token
@@ -494,9 +506,10 @@ def gdr_commit_path(k, v, g, beta, path, n_path, h0=None, ht=None, stream=None, 
             ht = torch.empty((B, HV, dk, dv), dtype=f32, device=k.device)
     elif ht is not h0:
         _given("ht", ht, (B, HV, dk, dv), f32, index)
-    st = lib.gdr_commit_path(k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), h0_ptr,
-                             ht.data_ptr(), path.data_ptr(), n_path.data_ptr(), B, T, HK, HV, dk,
-                             dv, max_path, _stream_of(stream, index), code, flags)
+    st = _on(index, lib.gdr_commit_path)(
+        k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), h0_ptr, ht.data_ptr(),
+        path.data_ptr(), n_path.data_ptr(), B, T, HK, HV, dk, dv, max_path,
+        _stream_of(stream, index), code, flags)
     if st != GDR_OK:
         _check(lib, st)
     return ht
@@ -527,8 +540,9 @@ def gdr_state_store(state, slots, cache, scale, stream=None):
     lib = load_library()
     N, n_slots, HV, dk, dv, index = _state_cache_sizes(slots, cache, scale)
     _given("state", state, (N, HV, dk, dv), torch.float32, index)
-    st = lib.gdr_state_store(state.data_ptr(), slots.data_ptr(), cache.data_ptr(),
-                             scale.data_ptr(), N, n_slots, HV, dk, dv, _stream_of(stream, index))
+    st = _on(index, lib.gdr_state_store)(
+        state.data_ptr(), slots.data_ptr(), cache.data_ptr(), scale.data_ptr(), N, n_slots, HV,
+        dk, dv, _stream_of(stream, index))
     if st != GDR_OK:
         _check(lib, st)
 
@@ -543,8 +557,9 @@ def gdr_state_load(cache, scale, slots, out=None, stream=None):
             out = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=cache.device)
     else:
         _given("out", out, (N, HV, dk, dv), torch.float32, index)
-    st = lib.gdr_state_load(cache.data_ptr(), scale.data_ptr(), slots.data_ptr(), out.data_ptr(),
-                            N, n_slots, HV, dk, dv, _stream_of(stream, index))
+    st = _on(index, lib.gdr_state_load)(
+        cache.data_ptr(), scale.data_ptr(), slots.data_ptr(), out.data_ptr(), N, n_slots, HV, dk,
+        dv, _stream_of(stream, index))
     if st != GDR_OK:
         _check(lib, st)
     return out
@@ -586,27 +601,25 @@ def gdr_forward_host(q, k, v, g, beta, h0, out, ht, chunk=64, stream=None, stagi
         if t is not None and (tuple(t.shape) != (B, HV, dk, dv) or t.dtype != torch.float32):
             raise ValueError("%s must be float32 [B, HV, dk, dv]" % name)
     dev = torch.device("cuda") if device is None else torch.device(device)
-    need = int(lib.gdr_host_staging_bytes(B, T, HK, HV, dk, dv, chunk, code))
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    need = int(_on(index, lib.gdr_host_staging_bytes)(B, T, HK, HV, dk, dv, chunk, code))
     if need > 0 and (staging is None or staging.numel() * staging.element_size() < need):
         with _memory_of(stream):
             staging = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     st_ptr = _ptr(staging) if need > 0 else None
     st_bytes = staging.numel() * staging.element_size() if need > 0 else 0
-    st = lib.gdr_forward_host(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0),
-                              _ptr(out), _ptr(ht), B, T, HK, HV, dk, dv, chunk,
-                              ctypes.c_void_p(stream.cuda_stream), code, st_ptr, st_bytes)
+    st = _on(index, lib.gdr_forward_host)(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out), _ptr(ht), B, T, HK,
+        HV, dk, dv, chunk, ctypes.c_void_p(_stream_of(stream, index)), code, st_ptr, st_bytes)
     _check(lib, st)
     return out, ht
 
 
 def gdr_device_check(stream=None):
-    """Waits for the stream and raises if a kernel reported a bounded-wait timeout."""
+    """Waits for the stream and raises if a kernel on its device reported a bounded-wait timeout."""
     lib = load_library()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    _check(lib, lib.gdr_device_check(ctypes.c_void_p(stream.cuda_stream)))
+    index = torch.cuda.current_device() if stream is None else stream.device.index
+    _check(lib, _on(index, lib.gdr_device_check)(ctypes.c_void_p(_stream_of(stream, index))))
 
 
 def gdr_trace_enable(on=True):

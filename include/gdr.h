@@ -41,6 +41,7 @@
  *
  * Streams and errors.  All work is enqueued on `stream` (a cudaStream_t; NULL
  * is the legacy default stream) and the calls return without waiting for it.
+ * The pointers and the stream belong to the current device (cudaSetDevice).
  * Argument errors are detected before anything is enqueued and leave every
  * output untouched.  GDR_ERR_CUDA means a CUDA runtime call or launch failed;
  * gdr_last_cuda_error() gives the cudaError_t code.  No call allocates device

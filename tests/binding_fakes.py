@@ -72,6 +72,7 @@ class Host:
         p(torch.cuda, "stream", lambda s: use("stream", s))
         p(torch.cuda, "device", lambda d: use("device", index_of(d)))
         p(torch.cuda, "current_device", lambda: host.device)
+        p(torch._C, "_cuda_getDevice", lambda: host.device)
         p(torch.cuda, "current_stream", lambda d=None: Stream(1000 + index_of(
             host.device if d is None else d), index_of(host.device if d is None else d)))
         p(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i)
