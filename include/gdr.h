@@ -484,18 +484,19 @@ GDR_API gdr_status gdr_commit_path(const void *k, const void *v, const float *g,
  *
  * gdr_state_store: a = the largest magnitude of the row; scale = a * (1 / 127)
  * and code = x * (127 * (1 / a)) rounded to the nearest whole number (ties to
- * even), each a float32 operation rounded to nearest.  A row with a <= 1e-30 is stored as
- * zeros with scale 0.  A row that holds an infinity or a NaN is stored as
- * zeros with scale NaN, so that it comes back as NaN and not as plausible
+ * even), each a float32 operation rounded to nearest.  A row with a <= 1e-30 is
+ * stored as zeros with scale 0.  A row that holds an infinity or a NaN is stored
+ * as zeros with scale NaN, so that it comes back as NaN and not as plausible
  * numbers.  A state whose slot is outside [0, n_slots - 1] is not stored;
  * the slots of one call must differ from each other.
  * gdr_state_load: state = code * scale; a state whose slot is outside
  * [0, n_slots - 1] is set to zero (a new sequence); a slot may be loaded
  * more than once.
- * The error of a value is at most half its row's scale, 1/254 of the row's
- * largest magnitude.  The rows are scaled one by one because each key
- * channel decays at its own rate; the states that the recurrence runs on
- * stay float32.
+ * A value comes back off by at most (1/2 + 2^-13) times its row's scale, of a
+ * row with a <= 1e-30 its magnitude (half a step, 1/127 of the row's
+ * largest magnitude, and the float32 roundings, which move a tie by less than
+ * 2^-13 of one).  The rows are scaled one by one because each key channel
+ * decays at its own rate; the states that the recurrence runs on stay float32.
  *
  * Supported: N >= 0, n_slots >= 0, HV >= 1, dk and dv in {32, 64, 128}.
  * state and cache 16-byte aligned, slots and scale 4-byte.  Errors as
