@@ -206,7 +206,7 @@ def gdr_forward(q, k, v, g, beta, h0=None, out=None, ht=None, chunk=64, stream=N
         raise ValueError("k must match q in shape and dtype; v must match q in dtype")
     if tuple(g.shape) == (B, T, HV):   # a scalar gate: one log-decay per token and head
         flags |= GDR_FLAG_SCALAR_GATE
-    elif tuple(g.shape) != (B, T, HV, dk):
+    elif flags & GDR_FLAG_SCALAR_GATE or tuple(g.shape) != (B, T, HV, dk):
         raise ValueError("g must be [B, T, HV, dk] (channelwise) or [B, T, HV] (scalar gate)")
     if tuple(v.shape[:2]) != (B, T) or tuple(beta.shape) != (B, T, HV):
         raise ValueError("inconsistent shapes")
@@ -308,7 +308,7 @@ def gdr_forward_varlen(q, k, v, g, beta, cu_seqlens, h0=None, out=None, ht=None,
         raise ValueError("k must match q in shape and dtype; v must match q in dtype")
     if tuple(g.shape) == (total, HV):   # a scalar gate
         flags |= GDR_FLAG_SCALAR_GATE
-    elif tuple(g.shape) != (total, HV, dk):
+    elif flags & GDR_FLAG_SCALAR_GATE or tuple(g.shape) != (total, HV, dk):
         raise ValueError("g must be [total, HV, dk] (channelwise) or [total, HV] (scalar gate)")
     if v.shape[0] != total or tuple(beta.shape) != (total, HV):
         raise ValueError("inconsistent shapes")
@@ -367,7 +367,7 @@ def gdr_forward_tree(q, k, v, g, beta, parent, h0=None, out=None, stream=None, w
         raise ValueError("k must match q in shape and dtype; v must match q in dtype")
     if tuple(g.shape) == (B, T, HV):   # a scalar gate
         flags |= GDR_FLAG_SCALAR_GATE
-    elif tuple(g.shape) != (B, T, HV, dk):
+    elif flags & GDR_FLAG_SCALAR_GATE or tuple(g.shape) != (B, T, HV, dk):
         raise ValueError("g must be [B, T, HV, dk] (channelwise) or [B, T, HV] (scalar gate)")
     if tuple(v.shape[:2]) != (B, T) or tuple(beta.shape) != (B, T, HV):
         raise ValueError("inconsistent shapes")
@@ -487,7 +487,7 @@ def gdr_commit_path(k, v, g, beta, path, n_path, h0=None, ht=None, stream=None, 
     _given("k", k, (B, T, HK, dk), k.dtype, index)
     _given("v", v, (B, T, HV, dv), k.dtype, index)
     _given("beta", beta, (B, T, HV), f32, index)
-    if g.dim() == 3:  # a scalar gate
+    if g.dim() == 3 or flags & GDR_FLAG_SCALAR_GATE:
         flags |= GDR_FLAG_SCALAR_GATE
         _given("g", g, (B, T, HV), f32, index)
     else:
