@@ -424,7 +424,8 @@ def gdr_verify_drafts(p, tokens, parent, coins, u, q=None, max_path=None, path=N
 
     p [B, T, V] (f32 or bf16): the target's distribution after each node; q the same shape and
     dtype: what the node's children were drawn from, or None where they were proposed.  Their
-    rows may be further apart than V (a slice of a padded tensor).  tokens, parent [B, T] int32,
+    rows may be further apart than V (a slice of a padded tensor; padded alike, or to multiples of
+    16 bytes, they are read fast).  tokens, parent [B, T] int32,
     node 0 the root; parent may have any strides (one tree for the batch: tree.expand(B, T)).
     coins [B, T] and u [B] f32 random numbers in [0, 1).  All on the GPU.
     Returns (path [B, max_path], n_path [B], next_token [B]), int32: the accepted nodes, -1

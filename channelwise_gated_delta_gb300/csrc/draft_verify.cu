@@ -20,9 +20,10 @@
 //
 // Measured on the device (chains of 8 nodes, f32 with q, 131,072 elements):
 // 64 trees 16.0 us, the 67 MB of their last rows at 4.2 TB/s (0.62 of a
-// copy's rate).  By time stamps 2 us go to the nodes and their elements, 0.5 to 3
-// to the walk, 8 to 9 to the rows, 1 to the totals and 1.3 to the search.  One
-// tree over 32,768 elements: 4.8 us.
+// copy's rate); bf16 13.0, f32 without q 11.6, bf16 without q 9.3.  By time
+// stamps 2 us go to the nodes and their elements, 0.5 to 3 to the walk, 8 to 9
+// to the rows, 1 to the totals and 1.3 to the search.  One tree over 32,768
+// elements: 4.8 us.
 #include <stdint.h>
 
 #include "common.cuh"
@@ -48,8 +49,9 @@ __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 // numbers runs at the FP64 pipe's rate (with it 64 trees took 27 us instead of
 // 18, that pipe two thirds of the time), so x is taken apart by float
 // operations, all of them exact: added to 2^23 and rounded towards zero, a
-// number below 2^23 leaves its whole part in the low bits of the sum.  floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x)
-// and lo the same of what is left of it.
+// number below 2^23 leaves its whole part in the low bits of the sum.
+// floor(2^40 x) = 2^20 hi + lo with hi = floor(2^20 x) and lo the same of what is
+// left of it.
 struct Mass {
     uint32_t hi = 0, lo = 0;  // of at most 64 elements: a warp's sums fit 32 bits
     __device__ __forceinline__ void add(float x) {
@@ -85,7 +87,10 @@ __device__ __forceinline__ float divided(float w, float mass) {
 // The weights of M elements after n refusals with q, given P in w and Q in x:
 // the residual of the last refusal that left something (P before any);
 // norm[s] is the mass of residual s, 0 where it had none.  All elements take
-// a refusal together, for the latency of the division.
+// a refusal together, for the latency of the division.  Every refusal starts from P
+// again, so that those of one node cost by the square of their number: one
+// tree over 30,000 elements, 1 / 4 / 16 / 64 / 511 siblings all refused: 4.4 / 15
+// / 115 / 1,490 / 89,300 us.
 template <int M>
 __device__ __forceinline__ void residuals(float (&w)[M], const float (&x)[M], const float *norm,
                                           int n) {
@@ -132,7 +137,8 @@ __device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x)
 __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 
 // Elements i0 .. i0 + VEC - 1 of a row one by one, 0 outside of it: for the
-// ends of a row, and for rows of q that do not lie to 16 bytes as p's do.
+// ends of a row, and for rows of q that do not lie to 16 bytes as p's do (64
+// chains over 131,072 elements: 36 us, 15 where they do).
 template <typename Tp>
 __device__ __forceinline__ uint4 load_elements(const Tp *row, int i0, int V) {
     constexpr int N = Vec<Tp>::N;
@@ -666,8 +672,12 @@ cudaError_t launch_clusters(const VerifyArgs &a, int c, cudaStream_t stream) {
 // cluster of SMs): 7 of 8 SMs are counted (2,000 elements, 64 trees: 10.3
 // with 8 CTAs each, 5.6 with 1).
 // Otherwise CTAs of 256 threads, two a SM, stream the rows, as many per tree as
-// fit the device at once with 2048 elements each (131,072 elements, 64 trees: 25.3 / 18.2 / 16.4 /
-// 20.7 with 1 / 2 / 4 / 8; one tree: 17.6 / 11.9 / 8.7 / 7.0).
+// the device's slots (two a SM) hold with 2048 elements each (131,072 elements, 64
+// trees: 25.3 / 18.2 / 16.4 / 20.7 with 1 / 2 / 4 / 8; one tree: 17.6 / 11.9 / 8.7 /
+// 7.0).  Powers of two leave slots empty in between, and at the last batch of a size
+// its clusters do not all find room at once: 32 / 38 trees with 8 CTAs each 11.1 / 17.2, 39
+// / 45 / 50 / 60 / 64 / 76 with 4 each 13.6 / 14.5 / 14.9 / 16.0 / 16.4 / 25.1, 77 with 2 each
+// 20.1.
 template <typename Tp, bool HAS_Q>
 cudaError_t launch_q(const VerifyArgs &a, cudaStream_t stream) {
     int dev = 0, sms = 0;

@@ -12,8 +12,11 @@
 //
 // Measured on the device: 64 x 32 heads of 128 x 128, paths of 1 to 8 nodes,
 // 50.2 us (277 MB at 5.5 TB/s, 0.81 of a copy's rate), of one node 45.7 us (0.86), of 64
-// nodes 283 us (0.29 us a head and node on an SM, bound by its FMA pipes); 64 x
-// 32 heads of 64 x 64, paths of 1 to 5 nodes, 17.7 us (4.0 TB/s).
+// nodes 283 us (0.29 us a head and node on an SM, bound by its FMA pipes).  With few
+// heads an SM their lengths do not even out: 16 x 32 heads 20.4 us (0.50 of a
+// copy's rate), of one node 13.6 us (0.74).  Other dims, paths of 1 to 5 nodes:
+// 64 x 32 heads of 64 x 64 18 us (0.57; 16 x 32 heads 0.41), of 128 x 64 30 us (0.68),
+// in f32 41 us (0.50).
 //
 // The kernel for heads other than 128 x 128: a warp owns 16 columns of a head's
 // state; lane (cq = lane % 4, rg = lane / 4) holds columns 4 cq .. 4 cq + 3 of
@@ -21,7 +24,10 @@
 // the rows stays inside the warp, and between the nodes no warp waits for
 // another.  The arithmetic is on pairs of columns (fma.rn.f32x2: two roundings
 // as by two fma).  k and exp(g) of a batch of nodes are staged in shared memory
-// as (k, k, a, a), the pairs' form.
+// as (k, k, a, a), the pairs' form.  What bounds it is a chain in front of every
+// tile (path length, path, nodes, with nothing of the next tile in flight).  The
+// next batch of nodes waits in registers; with f32 nodes and dk = 128 they do not all
+// fit beside the state (172 bytes of spills; dk = 64: 20, bf16 dk = 128: 12).
 #include <stdint.h>
 
 #include "common.cuh"
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
                            const int *__restrict__ n_path, int T, int HK, int HV, int max_path,
                            int nheads, int *dev_error) {
     constexpr int kProducers = Producers<Tin>::kWarps;
-    constexpr int kHalf = kSlotNodes / kProducers;  // nodes of a slot per producer warp
+    constexpr int kOwn = kSlotNodes / kProducers;  // nodes of a slot per producer warp
     extern __shared__ __align__(128) unsigned char smem_raw[];
     BulkShared &sh = *reinterpret_cast<BulkShared *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -337,11 +343,11 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
 
     if (warp >= kGroups * kGroupWarps) {
         // ---- producers of group grp: heads grp, grp + 2, ...
-        // Warp number `half` brings kHalf nodes of each slot; the first also
+        // Warp number `part` brings kOwn nodes of each slot; the first also
         // asks for the states and writes the slot's count.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Producers<Tin>::kRegs));
         const int producer = warp - kGroups * kGroupWarps;
-        const int grp = producer / kProducers, half = producer % kProducers;
+        const int grp = producer / kProducers, part = producer % kProducers;
         int next_state = grp;  // the group's next head whose state has not been asked for
         // Asks for the states of heads up to `upto`, waiting for their buffers,
         // and up to `may` where that needs no wait.  A buffer's barriers tell
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
         // worked through it.  Before the wait for the slot of a head's
         // nodes that is known for the head itself, after it for the next one.
         auto states = [&](int upto, int may) {
-            while (half == 0 && ok && h0 && next_state < my && next_state <= may) {
+            while (part == 0 && ok && h0 && next_state < my && next_state <= may) {
                 const int buf = next_state % kBufs, use = next_state / kBufs;
                 if (use > 0) {
                     const uint32_t parity = (uint32_t)(use - 1) & 1u;
@@ -383,8 +389,8 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
             return from + lane < max_path ? path[(size_t)bb * max_path + from + lane] : -1;
         };
         struct Nodes {
-            Raw4<Tin> k[kHalf], v[kHalf];
-            float4 g[kHalf];
+            Raw4<Tin> k[kOwn], v[kOwn];
+            float4 g[kOwn];
             float beta, gate;  // of node `lane`
             int count, last;
         };
@@ -402,8 +408,8 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
             x.last = x.count < kSlotNodes || at + kSlotNodes >= n;
             const size_t row = (size_t)b * T;
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) {
-                const int node = half * kHalf + c;
+            for (int c = 0; c < kOwn; ++c) {
+                const int node = part * kOwn + c;
                 const int t = __shfl_sync(0xffffffffu, entry, (at & 31) + node);
                 if (node < x.count) {
                     const size_t krow = (row + t) * HK + hk, vrow = (row + t) * HV + hv;
@@ -444,8 +450,8 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
             if (!ok) return;
             states(this_head, this_head + kGroups);
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) {
-                const int j = half * kHalf + c;
+            for (int c = 0; c < kOwn; ++c) {
+                const int j = part * kOwn + c;
                 const float gate = GS ? __shfl_sync(0xffffffffu, x.gate, j) : 0.f;
                 if (j < x.count) {
                     store4(&slot.k[j][4 * lane], x.k[c].f32());
@@ -460,8 +466,8 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
                     store4(&slot.a[j][4 * lane], a);
                 }
             }
-            if (lane / kHalf == half && lane < x.count) slot.beta[lane] = x.beta;
-            if (half == 0 && lane == 0) {
+            if (lane / kOwn == part && lane < x.count) slot.beta[lane] = x.beta;
+            if (part == 0 && lane == 0) {
                 slot.count = x.count;
                 slot.last = x.last;
             }
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(kBulkThreads<Tin>, 1)
             if (lane == 0) atomicOr(dev_error, 1);
             // never leave with loads in flight into this CTA: the last
             // states asked for, one per buffer at most
-            for (int i = next_state - kGroups, j = 0; half == 0 && h0 && i >= 0 && j < kBufs;
+            for (int i = next_state - kGroups, j = 0; part == 0 && h0 && i >= 0 && j < kBufs;
                  i -= kGroups, ++j)
                 sm100::mbar_wait_bounded(&sh.state_full[i % kBufs], (uint32_t)(i / kBufs) & 1u,
                                          kWaitNs);

@@ -422,18 +422,24 @@ GDR_API gdr_status gdr_forward_tree(const void *q, const void *k, const void *v,
  * with  sum_{j <= i} fix(w_j) > floor(m / 2^24 * sum_j fix(w_j)),  m =
  * floor(2^24 u).  Every other operation is one float32 operation, rounded
  * to nearest.  For p and q that sum to 1 the path and its next token are
- * distributed as tokens drawn from p one after another.  Sums of whole
+ * distributed as tokens drawn from p one after another; without q, rows that
+ * sum to s count as they are against M = 1, which is off by about |s - 1|
+ * (rounded to bf16, rows of 10^5 elements are 1 to within 2e-3).  Sums of whole
  * numbers do not depend on their order: the result is the same for every
  * split of the work, and so on every device.
+ * Fast are rows of p and q that lie alike to 16 bytes (ldp and ldq equal, or both
+ * multiples of 16 bytes; otherwise they are read element by element), and few
+ * refusals at one node with q: each is a pass over the node's rows, and the
+ * time of n of them grows with n^2.
  *
  * A node whose parent is not in [0, t - 1] or whose token is not in
  * [0, V - 1] is never accepted and changes nothing.  A coin or u that is NaN
  * counts as a refusal and as 0; u outside [0, 1) is clamped.  Supported:
  * B >= 0, 1 <= T <= 512, 1 <= V <= 2^22, 1 <= max_path <= T, ldp >= V,
  * ldq >= V, parent_sb and parent_st >= 0, prob_dtype GDR_F32 or GDR_BF16 (p
- * and q both); p and q 16-byte aligned, everything else 4-byte.  Errors: GDR_ERR_UNSUPPORTED for T > 512,
- * V > 2^22 or another dtype, GDR_ERR_SHAPE for the other limits, the rest as
- * gdr_forward_ex.
+ * and q both); p and q 16-byte aligned, everything else 4-byte.  Errors:
+ * GDR_ERR_UNSUPPORTED for T > 512, V > 2^22 or another dtype, GDR_ERR_SHAPE
+ * for the other limits, the rest as gdr_forward_ex.
  * Passage: none in the pages ("Support TreeUpdateSolve kernel",
  * trymirai/uzu PR #576, computes a draft tree's outputs; what a decoder does
  * with them is not in it).
