@@ -14,6 +14,7 @@ allocates are memory of that stream.
 """
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -30,6 +31,10 @@ GDR_FLAG_SCALAR_GATE = 4
 GDR_FLAG_NO_SEGMENTS = 8
 GDR_FLAG_TREE_BLOCKED = 0x10000
 GDR_FLAG_TREE_GRAM_PER_VALUE_HEAD = 0x20000
+GDR_FLAG_SILU = 0x40000
+GDR_FLAG_RMS_NORM = 0x80000
+GDR_FLAG_ROPE_INTERLEAVED = 0x100000
+GDR_FLAG_DT_SOFTPLUS = 0x200000
 
 
 def gdr_flag_segments(n):
@@ -47,7 +52,8 @@ EXPORTED = ("gdr_workspace_bytes", "gdr_set_workspace", "gdr_forward_ex", "gdr_f
             "gdr_forward_chunked_noalloc",
             "gdr_varlen_workspace_bytes", "gdr_forward_varlen", "gdr_tree_workspace_bytes",
             "gdr_forward_tree", "gdr_verify_drafts", "gdr_commit_path", "gdr_state_store",
-            "gdr_state_load", "gdr_host_staging_bytes", "gdr_forward_host", "gdr_device_check",
+            "gdr_state_load", "gdr_short_conv", "gdr_qk_norm", "gdr_ssm_workspace_bytes",
+            "gdr_ssm_forward", "gdr_host_staging_bytes", "gdr_forward_host", "gdr_device_check",
             "gdr_trace_enable", "gdr_trace_read", "gdr_status_string",
             "gdr_last_cuda_error", "gdr_version")
 
@@ -100,6 +106,15 @@ def load_library(path=LIB_PATH):
     lib.gdr_state_store.restype = i
     lib.gdr_state_load.argtypes = [vp] * 4 + [i] * 5 + [vp]
     lib.gdr_state_load.restype = i
+    lib.gdr_short_conv.argtypes = [vp] * 6 + [ip] + [i] * 4 + [ll] * 2 + [vp, i, u]
+    lib.gdr_short_conv.restype = i
+    f = ctypes.c_float
+    lib.gdr_qk_norm.argtypes = [vp] * 8 + [ll] + [i] * 4 + [ll] * 4 + [f] * 2 + [vp, i, u]
+    lib.gdr_qk_norm.restype = i
+    lib.gdr_ssm_workspace_bytes.argtypes = [ip] + [i] * 7 + [u]
+    lib.gdr_ssm_workspace_bytes.restype = sz
+    lib.gdr_ssm_forward.argtypes = [vp] * 11 + [ip] + [i] * 6 + [ll] * 4 + [vp, i, vp, sz, u]
+    lib.gdr_ssm_forward.restype = i
     lib.gdr_host_staging_bytes.argtypes = [i] * 8
     lib.gdr_host_staging_bytes.restype = sz
     lib.gdr_forward_host.argtypes = fwd + [vp, sz]
@@ -564,6 +579,234 @@ def gdr_state_load(cache, scale, slots, out=None, stream=None):
     if st != GDR_OK:
         _check(lib, st)
     return out
+
+
+def _rows_of(name, t, lead, inner, dtype, index):
+    """The distance in elements of the rows of ``t`` [*lead, *inner], a ``dtype`` tensor on CUDA
+    device ``index`` whose rows may lie further apart than they are wide."""
+    if t.get_device() != index or index < 0:
+        raise ValueError("%s must be a CUDA tensor%s"
+                         % (name, " on cuda:%d" % index if index >= 0 else ""))
+    if t.shape != lead + inner or t.dtype is not dtype:
+        raise ValueError("%s must be %s %s, got %s %s"
+                         % (name, dtype, list(lead + inner), t.dtype, list(t.shape)))
+    wide = 1
+    for n in inner:
+        wide *= n
+    if t.is_contiguous():
+        return wide
+    strides, want = t.stride(), 1
+    n = len(lead)
+    for size, stride in zip(reversed(inner), reversed(strides[n:])):
+        if size != 1 and stride != want:
+            raise ValueError("%s must have rows of adjacent elements" % name)
+        want *= size
+    ld = wide
+    if lead[-1] != 1:
+        ld = strides[n - 1]
+        if n == 2 and lead[0] > 1 and strides[0] != lead[1] * ld:
+            raise ValueError("%s must have its rows at one distance" % name)
+    elif n == 2 and lead[0] > 1:
+        ld = strides[0]
+    if ld < wide and t.numel():
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return max(ld, wide)
+
+
+def _sequences(lead, cu_seqlens):
+    """(offsets or None, N, T) of rows with the leading dimensions ``lead``."""
+    if cu_seqlens is None:
+        if len(lead) != 2:
+            raise ValueError("without cu_seqlens the tensors are [B, T, ...]")
+        return None, lead[0], lead[1]
+    if len(lead) != 1:
+        raise ValueError("with cu_seqlens the tensors are [rows, ...]")
+    cu, n = _cu_array(cu_seqlens)
+    if cu[n] != lead[0]:
+        raise ValueError("cu_seqlens[-1] (%d) != number of rows (%d)" % (cu[n], lead[0]))
+    return cu, n, 0
+
+
+def _optional(name, t, shape, index):
+    """The address of a float32 tensor of this shape, None for None."""
+    if t is None:
+        return None
+    _given(name, t, shape, torch.float32, index)
+    return t.data_ptr()
+
+
+def gdr_short_conv(x, weight, bias=None, cu_seqlens=None, s0=None, out=None, st=None, silu=True,
+                   stream=None, store_st=True):
+    """The causal convolution of each channel in front of a recurrence, with its state.
+
+    x [B, T, D], or packed [rows, D] with cu_seqlens (host ints [N + 1]), bf16 or f32; its rows
+    may lie further apart than D (part of a wider projection).  weight [D, W] f32, W 2 to 4 taps,
+    the last one the row's own; bias [D] f32 or None.  s0 [B, W - 1, D] in x's dtype: the rows in
+    front of each sequence, None for zeros; ``st=s0`` updates in place, ``store_st=False`` skips
+    the new state.  ``silu``: out = y / (1 + exp(-y)).  Returns (out, st), allocated when not given.
+    """
+    lib = load_library()
+    if x.dim() not in (2, 3) or weight.dim() != 2:
+        raise ValueError("x must be [B, T, D] or [rows, D] and weight [D, W]")
+    lead, D, index = tuple(x.shape[:-1]), x.shape[-1], x.get_device()
+    code = _dtype_code(x.dtype, "x")
+    ldx = _rows_of("x", x, lead, (D,), x.dtype, index)
+    cu, n, T = _sequences(lead, cu_seqlens)
+    W = weight.shape[1]
+    _given("weight", weight, (D, W), torch.float32, index)
+    state = (n, W - 1, D)
+    if s0 is not None:
+        _given("s0", s0, state, x.dtype, index)
+    with _memory_of(stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            ldo = D
+        else:
+            ldo = _rows_of("out", out, lead, (D,), x.dtype, index)
+        if st is None:
+            if store_st:
+                st = torch.empty((n, max(W - 1, 0), D), dtype=x.dtype, device=x.device)
+        elif st is not s0:
+            _given("st", st, state, x.dtype, index)
+    status = _on(index, lib.gdr_short_conv)(
+        x.data_ptr(), weight.data_ptr(), _optional("bias", bias, (D,), index),
+        None if s0 is None else s0.data_ptr(), out.data_ptr(),
+        None if st is None else st.data_ptr(), cu, n, T, D, W, ldx, ldo,
+        _stream_of(stream, index), code, GDR_FLAG_SILU if silu else 0)
+    if status != GDR_OK:
+        _check(lib, status)
+    return out, st
+
+
+def gdr_rope_freqs(d_rot, base=10000.0, inv_freq=None, device="cuda"):
+    """The frequencies of gdr_qk_norm for ``d_rot`` rotated channels, int64 [d_rot / 2] in 2^-64
+    turns a position: base^(-2 i / d_rot) radians for pair i, or ``inv_freq`` (radians a
+    position, one per pair)."""
+    if inv_freq is None:
+        inv_freq = [base ** (-2.0 * i / d_rot) for i in range(d_rot // 2)]
+    elif len(inv_freq) != d_rot // 2:
+        raise ValueError("inv_freq must have d_rot / 2 entries")
+    turns = [int(float(f) / (2.0 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for f in inv_freq]
+    return torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64,
+                        device=device)
+
+
+def gdr_qk_norm(q, k, weight_q=None, weight_k=None, positions=None, freqs=None, norm="l2",
+                eps=1e-6, q_scale=1.0, interleaved=False, out_q=None, out_k=None, stream=None):
+    """Norms of the heads of q and k, and the rotation of their first channels by position.
+
+    q [B, T, HQ, d] (or [rows, HQ, d]), k with HK heads, bf16 or f32; rows may lie apart (parts of
+    one projection).  ``norm``: "l2" (x / sqrt(sum x^2 + eps), as gdr_forward wants q and k) or
+    "rms" (mean x^2); weight_q, weight_k [d] f32 or None; q times ``q_scale``.  With ``freqs``
+    (gdr_rope_freqs) and ``positions`` (int32, one per row) the first 2 len(freqs) channels are
+    rotated, as pairs (i, i + half), or neighbours if ``interleaved``.  ``out_q=q`` and
+    ``out_k=k`` work in place.  Returns (out_q, out_k), allocated when not given."""
+    lib = load_library()
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        raise ValueError("q and k must be [B, T, H, d] or [rows, H, d]")
+    if norm not in ("l2", "rms"):
+        raise ValueError('norm must be "l2" or "rms"')
+    lead, index = tuple(q.shape[:-2]), q.get_device()
+    HQ, d = q.shape[-2:]
+    HK = k.shape[-2]
+    code = _dtype_code(q.dtype, "q and k")
+    ldq = _rows_of("q", q, lead, (HQ, d), q.dtype, index)
+    ldk = _rows_of("k", k, lead, (HK, d), q.dtype, index)
+    if (positions is None) != (freqs is None):
+        raise ValueError("a rotation needs positions and freqs")
+    d_rot = 0
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be [d_rot / 2]")
+        d_rot = 2 * freqs.shape[0]
+        _given("freqs", freqs, (d_rot // 2,), torch.int64, index)
+        _given("positions", positions, lead, torch.int32, index)
+    with _memory_of(stream):
+        if out_q is None:
+            out_q, ldoq = torch.empty(q.shape, dtype=q.dtype, device=q.device), HQ * d
+        else:
+            ldoq = _rows_of("out_q", out_q, lead, (HQ, d), q.dtype, index)
+        if out_k is None:
+            out_k, ldok = torch.empty(k.shape, dtype=q.dtype, device=q.device), HK * d
+        else:
+            ldok = _rows_of("out_k", out_k, lead, (HK, d), q.dtype, index)
+    rows = 1
+    for n in lead:
+        rows *= n
+    flags = (GDR_FLAG_RMS_NORM if norm == "rms" else 0) | (
+        GDR_FLAG_ROPE_INTERLEAVED if interleaved else 0)
+    status = _on(index, lib.gdr_qk_norm)(
+        q.data_ptr(), k.data_ptr(), _optional("weight_q", weight_q, (d,), index),
+        _optional("weight_k", weight_k, (d,), index), positions.data_ptr() if d_rot else None,
+        freqs.data_ptr() if d_rot else None, out_q.data_ptr(), out_k.data_ptr(), rows, HQ, HK, d,
+        d_rot, ldq, ldk, ldoq, ldok, eps, q_scale, _stream_of(stream, index), code, flags)
+    if status != GDR_OK:
+        _check(lib, status)
+    return out_q, out_k
+
+
+def gdr_ssm_workspace_bytes(B, T, HK, HV, dk, dv, dtype=torch.bfloat16, cu_seqlens=None, flags=0):
+    """Workspace of gdr_ssm_forward, of B sequences of T tokens or of those of ``cu_seqlens``."""
+    lib = load_library()
+    cu, n = (None, B) if cu_seqlens is None else _cu_array(cu_seqlens)
+    return int(lib.gdr_ssm_workspace_bytes(cu, n, T, HK, HV, dk, dv, _dtype_code(dtype), flags))
+
+
+def gdr_ssm_forward(x, b, c, dt, a, d=None, z=None, dt_bias=None, cu_seqlens=None, h0=None,
+                    out=None, ht=None, softplus=True, stream=None, workspace=None, flags=0,
+                    store_ht=True):
+    """The selective state space scan: S <- exp(step a) S + step b x^T, out = S^T c + d x, times
+    silu(z), with step = softplus(dt + dt_bias) (``softplus=False``: dt + dt_bias).
+
+    x, z [B, T, HV, dv]; b, c [B, T, HK, dk] (bf16 or f32, one dtype; rows may lie apart); dt
+    [B, T, HV] f32; a, d, dt_bias [HV] f32; with cu_seqlens (host ints [N + 1]) packed rows in
+    place of [B, T].  h0, ht [B, HV, dk, dv] f32 as in gdr_forward (``ht=h0`` updates in place;
+    ``store_ht=False`` skips it).  d, z, dt_bias, h0 may be None.  Returns (out, ht)."""
+    lib = load_library()
+    if x.dim() not in (3, 4) or b.dim() != x.dim():
+        raise ValueError("x and b must be [B, T, H, d] or [rows, H, d]")
+    lead, index = tuple(x.shape[:-2]), x.get_device()
+    HV, dv = x.shape[-2:]
+    HK, dk = b.shape[-2:]
+    code = _dtype_code(x.dtype, "x, b and c")
+    ldx = _rows_of("x", x, lead, (HV, dv), x.dtype, index)
+    ldb = _rows_of("b", b, lead, (HK, dk), x.dtype, index)
+    ldc = _rows_of("c", c, lead, (HK, dk), x.dtype, index)
+    ldz = 0 if z is None else _rows_of("z", z, lead, (HV, dv), x.dtype, index)
+    _given("dt", dt, lead + (HV,), torch.float32, index)
+    _given("a", a, (HV,), torch.float32, index)
+    cu, n, T = _sequences(lead, cu_seqlens)
+    state = (n, HV, dk, dv)
+    h0_ptr = _optional("h0", h0, state, index)
+    if softplus:
+        flags |= GDR_FLAG_DT_SOFTPLUS
+    need = int(_on(index, lib.gdr_ssm_workspace_bytes)(cu, n, T, HK, HV, dk, dv, code, flags))
+    with _memory_of(stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _given("out", out, x.shape, x.dtype, index)
+        if ht is None:
+            if store_ht:
+                ht = torch.empty(state, dtype=torch.float32, device=x.device)
+        elif ht is not h0:
+            _given("ht", ht, state, torch.float32, index)
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    ws, ws_bytes = None, 0
+    if need:
+        if workspace.get_device() != index:
+            raise ValueError("workspace must be a CUDA tensor on cuda:%d" % index)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = _on(index, lib.gdr_ssm_forward)(
+        x.data_ptr(), b.data_ptr(), c.data_ptr(), dt.data_ptr(), a.data_ptr(),
+        _optional("d", d, (HV,), index), None if z is None else z.data_ptr(),
+        _optional("dt_bias", dt_bias, (HV,), index), h0_ptr, out.data_ptr(),
+        None if ht is None else ht.data_ptr(), cu, n, T, HK, HV, dk, dv, ldx, ldb, ldc, ldz,
+        _stream_of(stream, index), code, ws, ws_bytes, flags)
+    if status != GDR_OK:
+        _check(lib, status)
+    return out, ht
 
 
 def gdr_host_staging_bytes(B, T, HK, HV, dk, dv, chunk=64, dtype=torch.bfloat16):

@@ -371,7 +371,9 @@ const char *kKernelNames[gdr::kNumKernels] = {"gdr_decode_kernel", "gdr_chunk_pr
                                               "gdr_tree_gram_kernel", "gdr_tree_solve_kernel",
                                               "gdr_chunk_scan_tc", "gdr_chunk_prep_tc",
                                               "gdr_verify_kernel", "gdr_commit_kernel",
-                                              "gdr_state_store_kernel", "gdr_state_load_kernel"};
+                                              "gdr_state_store_kernel", "gdr_state_load_kernel",
+                                              "gdr_short_conv_kernel", "gdr_qk_norm_kernel",
+                                              "gdr_ssm_kernel"};
 
 }  // namespace
 

@@ -80,7 +80,10 @@ enum KernelId {
     kKernCommit = 13,
     kKernStateStore = 14,
     kKernStateLoad = 15,
-    kNumKernels = 16
+    kKernShortConv = 16,
+    kKernQkNorm = 17,
+    kKernSsm = 18,
+    kNumKernels = 19
 };
 // Called by the launchers around each launch; no-ops unless tracing is on.
 void trace_begin(int kernel, cudaStream_t stream);

@@ -1,0 +1,231 @@
+// qk_norm.cu -- gdr_qk_norm: norms of the heads of q and k, with the rotation
+// of their first channels by the token's position in the same pass.
+//
+// A head of d values is held by d / 8 lanes, eight adjacent values each; the
+// sum of squares is a shuffle reduction, the partner of a rotated channel (d_rot
+// / 2 away, or its neighbour) another lane's value or the lane's own.  Every
+// value is read and written once: memory bounds it.
+//
+// Angles: a frequency is given in 2^-64 turns, and position times frequency
+// in 64-bit integers wraps at whole turns, so that the angle's reduction is
+// exact at any position; its top 32 bits as a float give sine and cosine to
+// float accuracy.  A warp forms them once for a token and uses them for the
+// heads that it walks.
+#include <stdint.h>
+
+#include "common.cuh"
+#include "gdr.h"
+#include "packed.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
+    const uint4 r = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+struct NormArgs {
+    const void *q, *k;
+    void *oq, *ok;
+    const float *wq, *wk;
+    const int *pos;
+    const unsigned long long *freq;
+    long long rows, ldq, ldk, ldoq, ldok;
+    int HQ, HK, d_rot;
+    int per_warp, parts;  // groups of heads a warp walks; warps of a row
+    float eps, q_scale, inv_n;
+};
+
+// ROT: 0 none, 1 channel i with i + d_rot / 2, 2 channel 2 i with 2 i + 1.
+template <typename T, int D, int ROT>
+__global__ void __launch_bounds__(32 * kWarps) gdr_qk_norm_kernel(const NormArgs a) {
+    constexpr int L = D / 8, G = 32 / L;  // lanes of a head, heads of a warp's step
+    const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
+    const long long w = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
+    const long long row = w / a.parts;
+    if (row >= a.rows) return;
+    const int c = 8 * l;
+
+    float cs[8], sn[8];  // of the channel's pair; interleaved: of pair i / 2
+    const int half = a.d_rot / 2;
+    const bool turned = ROT && c < a.d_rot, upper = ROT == 1 && c >= half;
+    if (ROT && turned) {
+        const long long p = a.pos[row];
+#pragma unroll
+        for (int e = 0; e < (ROT == 1 ? 8 : 4); ++e) {
+            const int i = ROT == 1 ? (upper ? c - half : c) + e : c / 2 + e;
+            const unsigned long long turn = (unsigned long long)p * __ldg(a.freq + i);
+            // the nearest 2^-32 of a turn, in half turns within [-1, 1)
+            const int t = (int)(unsigned)((turn + 0x80000000ull) >> 32);
+            sincospif((float)t * 0x1p-31f, &sn[e], &cs[e]);
+        }
+    }
+    const int from = upper ? l - half / 8 : l + half / 8;
+    const int partner = sub * L + (turned ? from : l);
+
+    const int nq = (a.HQ + G - 1) / G, nk = (a.HK + G - 1) / G;
+    const int g0 = (int)(w % a.parts) * a.per_warp, g1 = min(g0 + a.per_warp, nq + nk);
+    for (int g = g0; g < g1; ++g) {
+        const bool is_q = g < nq;
+        const int head = (is_q ? g : g - nq) * G + sub;
+        const bool on = head < (is_q ? a.HQ : a.HK);
+        float x[8];
+        if (on) {
+            const T *src = is_q ? static_cast<const T *>(a.q) + row * a.ldq
+                                : static_cast<const T *>(a.k) + row * a.ldk;
+            load8(src + head * D + c, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
+#pragma unroll
+        for (int off = L / 2; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        s = fmaf(s, a.inv_n, a.eps);
+        // a head of zeros without eps stays zeros
+        const float inv = s == 0.f ? 0.f : (is_q ? a.q_scale : 1.f) / sqrtf(s);
+        const float *wt = is_q ? a.wq : a.wk;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] *= inv;
+            if (wt) x[e] *= __ldg(wt + c + e);
+        }
+        if (ROT == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = __shfl_sync(0xffffffffu, x[e], partner);
+                if (turned) x[e] = upper ? fmaf(x[e], cs[e], y * sn[e]) : fmaf(x[e], cs[e], -y * sn[e]);
+            }
+        } else if (ROT == 2 && turned) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = x[2 * e], q = x[2 * e + 1];
+                x[2 * e] = fmaf(p, cs[e], -q * sn[e]);
+                x[2 * e + 1] = fmaf(q, cs[e], p * sn[e]);
+            }
+        }
+        if (on) {
+            T *dst = is_q ? static_cast<T *>(a.oq) + row * a.ldoq
+                          : static_cast<T *>(a.ok) + row * a.ldok;
+            store8(dst + head * D + c, x);
+        }
+    }
+}
+
+template <typename T, int D, int ROT>
+cudaError_t launch(NormArgs a, cudaStream_t stream) {
+    constexpr int G = 256 / D;
+    const int groups = (a.HQ + G - 1) / G + (a.HK + G - 1) / G;
+    // a warp walks all groups of a row where there are rows enough
+    int parts = 1;
+    while (parts < groups && a.rows * parts < 152 * 16) parts *= 2;
+    if (parts > groups) parts = groups;
+    a.per_warp = (groups + parts - 1) / parts;
+    a.parts = (groups + a.per_warp - 1) / a.per_warp;
+    const long long ctas = (a.rows * a.parts + kWarps - 1) / kWarps;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    trace_begin(kKernQkNorm, stream);
+    gdr_qk_norm_kernel<T, D, ROT><<<(unsigned)ctas, 32 * kWarps, 0, stream>>>(a);
+    trace_end(kKernQkNorm, stream);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t by_rotation(const NormArgs &a, bool interleaved, cudaStream_t s) {
+    if (a.d_rot == 0) return launch<T, D, 0>(a, s);
+    return interleaved ? launch<T, D, 2>(a, s) : launch<T, D, 1>(a, s);
+}
+
+template <typename T>
+cudaError_t by_dim(const NormArgs &a, int d, bool interleaved, cudaStream_t s) {
+    switch (d) {
+        case 32: return by_rotation<T, 32>(a, interleaved, s);
+        case 64: return by_rotation<T, 64>(a, interleaved, s);
+        case 128: return by_rotation<T, 128>(a, interleaved, s);
+        default: return by_rotation<T, 256>(a, interleaved, s);
+    }
+}
+
+}  // namespace
+}  // namespace gdr
+
+extern "C" GDR_API gdr_status gdr_qk_norm(const void *q, const void *k, const float *weight_q,
+                                          const float *weight_k, const int *positions,
+                                          const unsigned long long *freqs, void *out_q, void *out_k,
+                                          long long rows, int HQ, int HK, int d, int d_rot,
+                                          long long ldq, long long ldk, long long ldoq,
+                                          long long ldok, float eps, float q_scale, void *stream,
+                                          int dtype, unsigned flags) {
+    using namespace gdr;
+    if (rows < 0 || HQ <= 0 || HK <= 0 || !(eps >= 0.f)) return GDR_ERR_SHAPE;
+    if ((d != 32 && d != 64 && d != 128 && d != 256) || (dtype != GDR_F32 && dtype != GDR_BF16) ||
+        (flags & ~(GDR_FLAG_RMS_NORM | GDR_FLAG_ROPE_INTERLEAVED)))
+        return GDR_ERR_UNSUPPORTED;
+    if (d_rot < 0 || d_rot > d || d_rot % 16 != 0) return GDR_ERR_UNSUPPORTED;
+    const long long wq = (long long)HQ * d, wk = (long long)HK * d;
+    if (wq > 0x7fffffffLL || wk > 0x7fffffffLL || ldq < wq || ldk < wk || ldoq < wq || ldok < wk ||
+        !rows_fit(rows, ldq) || !rows_fit(rows, ldk) || !rows_fit(rows, ldoq) ||
+        !rows_fit(rows, ldok) || rows > (1LL << 40))
+        return GDR_ERR_SHAPE;
+    if (rows == 0) return GDR_OK;
+    if (!q || !k || !out_q || !out_k || (d_rot > 0 && (!positions || !freqs))) return GDR_ERR_NULL;
+    const int vec = dtype == GDR_BF16 ? 8 : 4;
+    const size_t es = dtype == GDR_BF16 ? 2 : 4;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(out_q) || !aligned16(out_k) ||
+        !aligned4(weight_q) || !aligned4(weight_k) || !aligned4(positions) ||
+        ((uintptr_t)freqs & 7u) || ldq % vec || ldk % vec || ldoq % vec || ldok % vec)
+        return GDR_ERR_ALIGN;
+    const RowSet in[2] = {{q, wq * es, ldq * es, rows}, {k, wk * es, ldk * es, rows}};
+    const RowSet out[2] = {{out_q, wq * es, ldoq * es, rows}, {out_k, wk * es, ldok * es, rows}};
+    const RowSet other[4] = {packed_rows(weight_q, d * 4), packed_rows(weight_k, d * 4),
+                             d_rot ? packed_rows(positions, rows * 4) : RowSet{},
+                             d_rot ? packed_rows(freqs, d_rot / 2 * 8) : RowSet{}};
+    if (rows_overlap(out[0], out[1])) return GDR_ERR_ALIAS;
+    for (int i = 0; i < 2; ++i) {
+        for (int j = 0; j < 2; ++j) {
+            const bool in_place = i == j && in[j].p == out[i].p && in[j].ld == out[i].ld;
+            if (!in_place && rows_overlap(out[i], in[j])) return GDR_ERR_ALIAS;
+        }
+        for (int j = 0; j < 4; ++j)
+            if (rows_overlap(out[i], other[j])) return GDR_ERR_ALIAS;
+    }
+    const NormArgs a = {q, k, out_q, out_k, weight_q, weight_k, positions, freqs, rows, ldq, ldk,
+                        ldoq, ldok, HQ, HK, d_rot, 0, 0, eps, q_scale,
+                        (flags & GDR_FLAG_RMS_NORM) ? 1.f / d : 1.f};
+    const bool il = (flags & GDR_FLAG_ROPE_INTERLEAVED) != 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == GDR_BF16 ? by_dim<__nv_bfloat16>(a, d, il, s)
+                                            : by_dim<float>(a, d, il, s);
+    if (e == cudaSuccess) return GDR_OK;
+    record_cuda_error(e);
+    return GDR_ERR_CUDA;
+}

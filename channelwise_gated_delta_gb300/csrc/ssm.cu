@@ -1,0 +1,296 @@
+// ssm.cu -- gdr_ssm_forward: the selective state space recurrence on states
+// [dk][dv], per token
+//     step = softplus(dt + dt_bias),  S <- exp(step A) S + step b x^T,
+//     out = S^T c + D x, times silu(z).
+//
+// gdr_ssm_walk_kernel runs it token by token, in float32 throughout, for
+// every type and size.  One CTA per (unit of a sequence, value head, 32
+// columns); warp w holds the rows w dk / 4 .. of the columns of its lanes in
+// registers, so that a token is three operations an element of the state and
+// no exchange: the four warps' partial outputs meet in shared memory once
+// every kTok tokens.  A single token is one pass over the state, bound by
+// memory; a long walk is bound by its operations.
+#include <limits.h>
+#include <stdint.h>
+
+#include "gdr.h"
+#include "ssm.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kTok = 16;
+constexpr int kThreads = 128;
+constexpr int kCols = 32;
+
+template <typename T, int DK, int PASS>
+__global__ void __launch_bounds__(kThreads)
+    gdr_ssm_walk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SeqTable table) {
+    constexpr int R = DK / 4;  // rows of a warp
+    __shared__ __align__(16) float sb[kTok][DK], sc[kTok][DK];
+    __shared__ float sx[kTok][kCols], part[4][kTok][kCols], sstep[kTok], sdec[kTok], slog[kTok];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tiles = a.dv / kCols;
+    const int tile = blockIdx.x % tiles, rest = blockIdx.x / tiles;
+    const int hv = rest % a.HV, hk = hv / (a.HV / a.HK);
+    const SeqUnit u = find_unit(table, rest / a.HV);
+    const int unit = table.unit0 + rest / a.HV;
+    const long long cut = a.seg_rows;
+    const int t0 = (int)(u.unit * cut), t1 = (int)min((long long)u.len, t0 + cut);
+    if (PASS == 1 && t1 == u.len) return;  // no unit follows
+    const int col = tile * kCols + lane;
+    const size_t per = (size_t)DK * a.dv;
+
+    float S[R];
+    const size_t at = (size_t)(warp * R) * a.dv + col;
+#pragma unroll
+    for (int r = 0; r < R; ++r) S[r] = 0.f;
+    if (a.h0 && u.unit == 0) {
+        const float *h = a.h0 + ((size_t)u.seq * a.HV + hv) * per + at;
+#pragma unroll
+            for (int r = 0; r < R; ++r) S[r] = h[(size_t)r * a.dv];
+    }
+    if (PASS == 2)
+        for (int i = 0; i < u.unit; ++i) {
+            const size_t s = (size_t)(unit - u.unit + i) * a.HV + hv;
+            const float keep = expf(a.seg_log[s]);
+            const float *e = a.seg_state + s * per + at;
+#pragma unroll
+            for (int r = 0; r < R; ++r) S[r] = fmaf(keep, S[r], e[(size_t)r * a.dv]);
+        }
+
+    const T *x = static_cast<const T *>(a.x) + u.row0 * a.ldx + (size_t)hv * a.dv + tile * kCols;
+    const T *b = static_cast<const T *>(a.b) + u.row0 * a.ldb + (size_t)hk * DK;
+    const T *c = static_cast<const T *>(a.c) + u.row0 * a.ldc + (size_t)hk * DK;
+    const float *dt = a.dt + u.row0 * a.HV + hv;
+    const float A = a.A[hv], bias = a.dt_bias ? a.dt_bias[hv] : 0.f, D = a.D ? a.D[hv] : 0.f;
+    float total = 0.f;
+
+    constexpr int NB = kTok * DK / kThreads, NX = kTok * kCols / kThreads;
+    float rb[NB], rc[NB], rx[NX], rdt = 0.f;
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int e = tid + kThreads * i, k = e / DK, ch = e % DK;
+            const bool in = t + k < t1;
+            rb[i] = in ? to_f32(b[(t + k) * a.ldb + ch]) : 0.f;
+            rc[i] = in && PASS != 1 ? to_f32(c[(t + k) * a.ldc + ch]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int k = (tid + kThreads * i) / kCols;
+            rx[i] = t + k < t1 ? to_f32(x[(t + k) * a.ldx + lane]) : 0.f;
+        }
+        if (tid < kTok && t + tid < t1) rdt = dt[(long long)(t + tid) * a.HV];
+    };
+    fetch(t0);
+    for (int t = t0; t < t1; t += kTok) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int e = tid + kThreads * i;
+            sb[e / DK][e % DK] = rb[i];
+            sc[e / DK][e % DK] = rc[i];
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) sx[(tid + kThreads * i) / kCols][lane] = rx[i];
+        if (tid < kTok) {
+            const float step = t + tid < t1 ? ssm_step(rdt, bias, a.softplus) : 0.f;
+            sstep[tid] = step;
+            slog[tid] = step * A;
+            sdec[tid] = expf(step * A);
+        }
+        __syncthreads();
+        if (t + kTok < t1) fetch(t + kTok);
+        const int n = min(kTok, t1 - t);
+#pragma unroll 2
+        for (int k = 0; k < n; ++k) {
+            const float keep = sdec[k], xs = sstep[k] * sx[k][lane];
+            if (PASS == 1) total += slog[k];
+            float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+                const float4 bv = *reinterpret_cast<const float4 *>(&sb[k][warp * R + r]);
+                S[r] = fmaf(keep, S[r], bv.x * xs);
+                S[r + 1] = fmaf(keep, S[r + 1], bv.y * xs);
+                S[r + 2] = fmaf(keep, S[r + 2], bv.z * xs);
+                S[r + 3] = fmaf(keep, S[r + 3], bv.w * xs);
+                if (PASS != 1) {
+                    const float4 cv = *reinterpret_cast<const float4 *>(&sc[k][warp * R + r]);
+                    y0 = fmaf(cv.x, S[r], y0);
+                    y1 = fmaf(cv.y, S[r + 1], y1);
+                    y0 = fmaf(cv.z, S[r + 2], y0);
+                    y1 = fmaf(cv.w, S[r + 3], y1);
+                }
+            }
+            if (PASS != 1) part[warp][k][lane] = y0 + y1;
+        }
+        __syncthreads();
+        if (PASS != 1) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int k = (tid + kThreads * i) / kCols;
+                if (k >= n) continue;
+                float y = (part[0][k][lane] + part[1][k][lane]) + (part[2][k][lane] + part[3][k][lane]);
+                y = fmaf(D, sx[k][lane], y);
+                const size_t row = (size_t)(u.row0 + t + k);
+                const size_t o = (size_t)hv * a.dv + col;
+                if (a.z) y = ssm_gate(y, to_f32(static_cast<const T *>(a.z)[row * a.ldz + o]));
+                static_cast<T *>(a.out)[row * a.HV * a.dv + o] = from_f32<T>(y);
+            }
+            __syncthreads();
+        }
+    }
+    float *end = nullptr;
+    if (PASS == 1) {
+        const size_t s = (size_t)unit * a.HV + hv;
+        end = a.seg_state + s * per;
+        if (tid == 0 && tile == 0) a.seg_log[s] = total;
+    } else if (a.ht && t1 == u.len) {
+        end = a.ht + ((size_t)u.seq * a.HV + hv) * per;
+    }
+    if (end)
+#pragma unroll
+        for (int r = 0; r < R; ++r) end[at + (size_t)r * a.dv] = S[r];
+}
+
+template <typename T, int DK, int PASS>
+cudaError_t launch_walk(const SsmArgs &a, cudaStream_t stream) {
+    return for_sequences(a.cu, a.N, a.T, a.seg_rows, [&](const SeqTable &t, long long units) {
+        const long long ctas = units * a.HV * (a.dv / kCols);
+        if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        trace_begin(kKernSsm, stream);
+        gdr_ssm_walk_kernel<T, DK, PASS><<<(unsigned)ctas, kThreads, 0, stream>>>(a, t);
+        trace_end(kKernSsm, stream);
+        return cudaGetLastError();
+    });
+}
+template <typename T, int DK>
+cudaError_t by_pass(const SsmArgs &a, int pass, cudaStream_t s) {
+    return pass == 0 ? launch_walk<T, DK, 0>(a, s)
+                     : pass == 1 ? launch_walk<T, DK, 1>(a, s) : launch_walk<T, DK, 2>(a, s);
+}
+template <typename T>
+cudaError_t by_dk(const SsmArgs &a, int pass, cudaStream_t s) {
+    return a.dk == 32 ? by_pass<T, 32>(a, pass, s)
+                      : a.dk == 64 ? by_pass<T, 64>(a, pass, s) : by_pass<T, 128>(a, pass, s);
+}
+
+struct Plan {
+    int seg_rows;      // INT_MAX: walks are not cut
+    long long units;   // units of the batch
+    size_t bytes;      // workspace
+    size_t off_log, off_h0;
+};
+
+Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, unsigned flags) {
+    Plan p = {INT_MAX, N, 0, 0, 0};
+    const int forced = (int)((flags >> 8) & 0xffu);
+    int longest = cu ? 0 : T;
+    for (int n = 0; cu && n < N; ++n) longest = longest > cu[n + 1] - cu[n] ? longest : cu[n + 1] - cu[n];
+    if (forced >= 2 && !(flags & GDR_FLAG_NO_SEGMENTS) && longest > 64) {
+        const int rows = ((longest + forced - 1) / forced + 63) / 64 * 64;
+        if (rows < longest) p.seg_rows = rows;
+    }
+    if (p.seg_rows != INT_MAX) {
+        p.units = count_units(cu, N, T, p.seg_rows);
+        const size_t state = (size_t)HV * dk * dv * 4;
+        p.off_log = p.units * state;
+        p.off_h0 = (p.off_log + (size_t)p.units * HV * 4 + 255) / 256 * 256;
+        p.bytes = p.off_h0 + (size_t)N * state;
+    }
+    return p;
+}
+
+gdr_status check_shape(const int *cu, int N, int T, int HK, int HV, int dk, int dv, int dtype,
+                       unsigned flags) {
+    if (N < 0 || (!cu && T < 0) || HK <= 0 || HV <= 0 || HV % HK) return GDR_ERR_SHAPE;
+    if (!supported_dim(dk) || !supported_dim(dv) || (dtype != GDR_F32 && dtype != GDR_BF16) ||
+        (flags & ~(GDR_FLAG_DT_SOFTPLUS | GDR_FLAG_FORCE_GENERIC | GDR_FLAG_NO_SEGMENTS | 0xff00u)))
+        return GDR_ERR_UNSUPPORTED;
+    if (N > 0 && cu && check_offsets(cu, N) != GDR_OK) return GDR_ERR_SHAPE;
+    // heads of the states, CTAs of a launch and element offsets
+    if ((long long)N * HV > (1LL << 28) || (long long)HV * dv > 0x7fffffffLL ||
+        (long long)HK * dk > 0x7fffffffLL)
+        return GDR_ERR_SHAPE;
+    return GDR_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_walk(const SsmArgs &a, int pass, cudaStream_t stream) {
+    return a.bf16 ? by_dk<__nv_bfloat16>(a, pass, stream) : by_dk<float>(a, pass, stream);
+}
+
+}  // namespace gdr
+
+extern "C" GDR_API size_t gdr_ssm_workspace_bytes(const int *cu_seqlens, int N, int T, int HK,
+                                                  int HV, int dk, int dv, int dtype,
+                                                  unsigned flags) {
+    using namespace gdr;
+    if (check_shape(cu_seqlens, N, T, HK, HV, dk, dv, dtype, flags) != GDR_OK || N == 0) return 0;
+    return make_plan(cu_seqlens, N, T, HV, dk, dv, flags).bytes;
+}
+
+extern "C" GDR_API gdr_status gdr_ssm_forward(
+    const void *x, const void *b, const void *c, const float *dt, const float *A, const float *D,
+    const void *z, const float *dt_bias, const float *h0, void *out, float *ht,
+    const int *cu_seqlens, int N, int T, int HK, int HV, int dk, int dv, long long ldx,
+    long long ldb, long long ldc, long long ldz, void *stream, int dtype, void *workspace,
+    size_t workspace_bytes, unsigned flags) {
+    using namespace gdr;
+    gdr_status st = check_shape(cu_seqlens, N, T, HK, HV, dk, dv, dtype, flags);
+    if (st != GDR_OK) return st;
+    const long long wx = (long long)HV * dv, wb = (long long)HK * dk;
+    const long long total = N == 0 ? 0 : cu_seqlens ? cu_seqlens[N] : (long long)N * T;
+    if (ldx < wx || ldb < wb || ldc < wb || (z && ldz < wx) || !rows_fit(total, ldx) ||
+        !rows_fit(total, ldb) || !rows_fit(total, ldc) || (z && !rows_fit(total, ldz)))
+        return GDR_ERR_SHAPE;
+    if (N == 0) return GDR_OK;
+    if (!A || (total > 0 && (!x || !b || !c || !dt || !out))) return GDR_ERR_NULL;
+    if (total == 0 && !ht) return GDR_OK;
+    const size_t es = dtype == GDR_BF16 ? 2 : 4;
+    const uintptr_t any = (uintptr_t)x | (uintptr_t)b | (uintptr_t)c | (uintptr_t)z;
+    if ((any & (es - 1)) || !aligned4(dt) || !aligned4(A) || !aligned4(D) || !aligned4(dt_bias) ||
+        !aligned16(out) || !aligned16(h0) || !aligned16(ht))
+        return GDR_ERR_ALIGN;
+    const size_t state = (size_t)HV * dk * dv * 4;
+    const RowSet o = packed_rows(out, total * wx * es), e = packed_rows(ht, N * state);
+    const RowSet in[] = {{x, wx * es, ldx * es, total}, {b, wb * es, ldb * es, total},
+                         {c, wb * es, ldc * es, total}, {z, wx * es, ldz * es, total},
+                         packed_rows(dt, total * HV * 4), packed_rows(A, (size_t)HV * 4),
+                         packed_rows(D, (size_t)HV * 4), packed_rows(dt_bias, (size_t)HV * 4)};
+    const RowSet h = packed_rows(h0, N * state);
+    for (const RowSet &r : in)
+        if (rows_overlap(o, r) || rows_overlap(e, r)) return GDR_ERR_ALIAS;
+    if (rows_overlap(o, h) || rows_overlap(o, e) || (h0 != ht && rows_overlap(e, h)))
+        return GDR_ERR_ALIAS;
+    const Plan plan = make_plan(cu_seqlens, N, T, HV, dk, dv, flags);
+    if (plan.bytes) {
+        if (!workspace || workspace_bytes < plan.bytes) return GDR_ERR_WORKSPACE;
+        if ((uintptr_t)workspace & 255u) return GDR_ERR_ALIGN;
+    }
+    if (plan.units * HV * (dv / 32) > 0x7fffffffLL) return GDR_ERR_SHAPE;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    SsmArgs a = {x, b, c, z, dt, A, D, dt_bias, h0, out, ht, nullptr, nullptr, ldx, ldb, ldc, ldz,
+                 N, T, HK, HV, dk, dv, cu_seqlens, plan.seg_rows,
+                 (flags & GDR_FLAG_DT_SOFTPLUS) ? 1 : 0, dtype == GDR_BF16 ? 1 : 0};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    if (plan.bytes) {
+        a.seg_state = reinterpret_cast<float *>(ws);
+        a.seg_log = reinterpret_cast<float *>(ws + plan.off_log);
+        if (h0 && h0 == ht) {
+            // a sequence's last unit may write ht before its first one has read h0
+            float *copy = reinterpret_cast<float *>(ws + plan.off_h0);
+            err = cudaMemcpyAsync(copy, h0, N * state, cudaMemcpyDeviceToDevice, s);
+            a.h0 = copy;
+        }
+        if (err == cudaSuccess) err = launch_ssm_walk(a, 1, s);
+        if (err == cudaSuccess) err = launch_ssm_walk(a, 2, s);
+    } else {
+        err = launch_ssm_walk(a, 0, s);
+    }
+    if (err == cudaSuccess) return GDR_OK;
+    record_cuda_error(err);
+    return GDR_ERR_CUDA;
+}

@@ -516,6 +516,115 @@ GDR_API gdr_status gdr_state_load(const signed char *cache, const float *scale, 
                                   void *stream);
 
 /*
+ * What stands around the recurrence in a layer: the short convolution in front
+ * of q, k and v, the norms (and rotation) of q and k, and the other recurrence
+ * on matrix states, the selective state space scan.  All three take dense
+ * batches (cu_seqlens NULL: N sequences of T rows) or packed ones (cu_seqlens
+ * as in gdr_forward_varlen, T ignored; gdr_qk_norm has only rows).  The offsets
+ * travel with the launches, at most 256 sequences each: nothing is copied from
+ * host memory, and every call can be captured into a graph.  Rows of the inputs
+ * may lie further apart than they are wide (parts of a wider projection):
+ * ldx and so on are the distances of rows in elements.  Such rows may lie
+ * between those of an output at the same distance; any other overlap of an
+ * output with another argument, but for those named below, is GDR_ERR_ALIAS.
+ * Passage: none in the pages, for any of the three.
+ *
+ * gdr_short_conv: a causal convolution of each channel with W taps,
+ *     out[t][c] = act(bias[c] + sum_j w[c][j] x[t - W + 1 + j][c]),
+ * act = silu(y) = y / (1 + exp(-y)) with GDR_FLAG_SILU, else nothing.
+ *
+ *   x, out      [rows][D], rows ldx and ldo elements apart, dtype
+ *   w, bias     float32 [D][W] and [D]; bias may be NULL
+ *   s0, st      [N][W - 1][D], dtype: the rows in front of each sequence,
+ *               oldest first (NULL: zeros), and those that the next call
+ *               needs (NULL: not stored).  st == s0 replaces them in place;
+ *               a sequence without rows keeps its state
+ *
+ * A sum is formed in float32 and rounded once.  Supported: D >= 1, W in
+ * {2, 3, 4}, ldx, ldo >= D, D below 2^23; x, out, s0 and st aligned to their
+ * elements, w and bias 4-byte.  Fast (16 bytes at a time) where those four are
+ * 16-byte aligned and D, ldx and ldo multiples of 16 bytes.  flags:
+ * GDR_FLAG_SILU or 0.
+ */
+#define GDR_FLAG_SILU 0x40000u
+GDR_API gdr_status gdr_short_conv(const void *x, const float *w, const float *bias, const void *s0,
+                                  void *out, void *st, const int *cu_seqlens, int N, int T, int D,
+                                  int W, long long ldx, long long ldo, void *stream, int dtype,
+                                  unsigned flags);
+
+/*
+ * gdr_qk_norm: each head x of d values of q and k by itself becomes
+ *     y = x / sqrt(sum x^2 + eps)      (GDR_FLAG_RMS_NORM: mean x^2),
+ * times weight[i] per channel, q times q_scale; a head whose sum and eps are 0
+ * becomes zeros.  Then, if d_rot > 0, the first d_rot channels are rotated:
+ * pair i (0 <= i < d_rot / 2) of channels i and i + d_rot / 2, or 2 i and
+ * 2 i + 1 with GDR_FLAG_ROPE_INTERLEAVED, by the angle a = positions[row] *
+ * freqs[i]:  (p, q) -> (p cos a - q sin a, q cos a + p sin a).
+ *
+ *   q, k, out_q, out_k  [rows][HQ][d] and [rows][HK][d], rows ld* elements apart,
+ *               dtype; out_q == q (at the same distance) and out_k == k are in place
+ *   weight_q, weight_k  float32 [d], or NULL
+ *   positions   int32 [rows] (not read if d_rot is 0)
+ *   freqs       uint64 [d_rot / 2]: each pair's turn a position, in 2^-64 turns.
+ *               Position times frequency wraps at whole turns, so that the angle of
+ *               a far position is as exact as that of a near one
+ *
+ * Computed in float32 and rounded once.  The sum of squares of a head has to
+ * fit float32 (a head beyond that comes out as zeros).  Supported: rows >= 0,
+ * HQ, HK >= 1, d in {32, 64, 128, 256}, d_rot <= d a multiple of 16, eps >= 0.
+ * Tensors 16-byte aligned and ld* multiples of 16 bytes, weights and positions
+ * 4-byte, freqs 8-byte aligned.  flags: the two above or 0.
+ */
+#define GDR_FLAG_RMS_NORM 0x80000u
+#define GDR_FLAG_ROPE_INTERLEAVED 0x100000u
+GDR_API gdr_status gdr_qk_norm(const void *q, const void *k, const float *weight_q,
+                               const float *weight_k, const int *positions,
+                               const unsigned long long *freqs, void *out_q, void *out_k,
+                               long long rows, int HQ, int HK, int d, int d_rot, long long ldq,
+                               long long ldk, long long ldoq, long long ldok, float eps,
+                               float q_scale, void *stream, int dtype, unsigned flags);
+
+/*
+ * gdr_ssm_forward: the selective state space scan.  Each value head keeps a
+ * float32 state S[dk][dv]; every token, in order,
+ *     step = softplus(dt + dt_bias)      (without GDR_FLAG_DT_SOFTPLUS: dt + dt_bias),
+ *     S   <- exp(step A) S + step b x^T,
+ *     out  = S^T c + D x,  times silu(z) if z is given.
+ * Value head hv reads b and c of head hv / (HV / HK), as in gdr_forward; a
+ * state is laid out as gdr_forward's (dk rows of dv), so gdr_state_store and
+ * gdr_state_load keep it as well.
+ *
+ *   x, z        [rows][HV][dv], rows ldx and ldz elements apart, dtype; z may be NULL
+ *   b, c        [rows][HK][dk], rows ldb and ldc elements apart, dtype
+ *   dt          float32 [rows][HV]
+ *   A           float32 [HV] (<= 0 expected, not checked), D, dt_bias float32 [HV] or NULL
+ *   h0, ht      [N][HV][dk][dv] float32, or NULL, as in gdr_forward
+ *               (ht == h0 updates in place; a sequence without rows copies)
+ *   out         [rows][HV][dv], dtype
+ *
+ * Sequences, rows and limits as above; HV % HK == 0, dk and dv in {32, 64,
+ * 128}.  x, b, c and z aligned to their elements, out, h0 and ht 16-byte, the
+ * rest 4-byte.  The state is float32 throughout; an output is rounded once.
+ *
+ * `workspace`: device memory of gdr_ssm_workspace_bytes(...) bytes, 256-byte
+ * aligned, untouched by anything else until the stream has passed the call;
+ * NULL where that is 0.  It is needed where long walks are cut into segments
+ * (GDR_FLAG_SEGMENTS(n): into at most n; GDR_FLAG_NO_SEGMENTS: never); the results agree to float32 rounding.
+ * GDR_FLAG_FORCE_GENERIC: token by token on CUDA cores whatever the route
+ * (for tests).  Errors as gdr_forward_ex.
+ */
+#define GDR_FLAG_DT_SOFTPLUS 0x200000u
+GDR_API size_t gdr_ssm_workspace_bytes(const int *cu_seqlens, int N, int T, int HK, int HV, int dk,
+                                       int dv, int dtype, unsigned flags);
+GDR_API gdr_status gdr_ssm_forward(const void *x, const void *b, const void *c, const float *dt,
+                                   const float *A, const float *D, const void *z,
+                                   const float *dt_bias, const float *h0, void *out, float *ht,
+                                   const int *cu_seqlens, int N, int T, int HK, int HV, int dk,
+                                   int dv, long long ldx, long long ldb, long long ldc,
+                                   long long ldz, void *stream, int dtype, void *workspace,
+                                   size_t workspace_bytes, unsigned flags);
+
+/*
  * Passage: none in the pages (error reporting of the bounded waits).
  * Waits for `stream`, then reads and clears the library's device error word
  * on the current device.  Returns GDR_ERR_TIMEOUT if a kernel gave up on a
