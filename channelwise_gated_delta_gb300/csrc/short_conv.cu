@@ -77,7 +77,9 @@ struct Vec<__nv_bfloat16, 1> {
 // y / (1 + e^-y)
 __device__ __forceinline__ float silu(float y) {
     constexpr float kLog2e = 1.4426950408889634f;
-    return y * __frcp_rn(1.f + sm100::fast_exp2(-kLog2e * y));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + sm100::fast_exp2(-kLog2e * y)));
+    return y * r;
 }
 
 template <typename T, int W, int VEC, bool SILU>

@@ -176,6 +176,7 @@ cudaError_t by_dk(const SsmArgs &a, int pass, cudaStream_t s) {
 }
 
 struct Plan {
+    int longest;       // rows of the longest sequence
     int seg_rows;      // INT_MAX: walks are not cut
     long long units;   // units of the batch
     size_t bytes;      // workspace
@@ -183,9 +184,9 @@ struct Plan {
 };
 
 Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, unsigned flags) {
-    Plan p = {INT_MAX, N, 0, 0, 0};
+    Plan p = {cu ? 0 : T, INT_MAX, N, 0, 0, 0};
     const int forced = (int)((flags >> 8) & 0xffu);
-    int longest = cu ? 0 : T;
+    int &longest = p.longest;
     for (int n = 0; cu && n < N; ++n) longest = longest > cu[n + 1] - cu[n] ? longest : cu[n + 1] - cu[n];
     if (forced >= 2 && !(flags & GDR_FLAG_NO_SEGMENTS) && longest > 64) {
         const int rows = ((longest + forced - 1) / forced + 63) / 64 * 64;
@@ -274,6 +275,9 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
     SsmArgs a = {x, b, c, z, dt, A, D, dt_bias, h0, out, ht, nullptr, nullptr, ldx, ldb, ldc, ldz,
                  N, T, HK, HV, dk, dv, cu_seqlens, plan.seg_rows,
                  (flags & GDR_FLAG_DT_SOFTPLUS) ? 1 : 0, dtype == GDR_BF16 ? 1 : 0};
+    const auto walk = plan.longest > 1 && !(flags & GDR_FLAG_FORCE_GENERIC) && ssm_chunks_supported(a)
+                          ? launch_ssm_chunks
+                          : launch_ssm_walk;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
     if (plan.bytes) {
@@ -285,10 +289,10 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
             err = cudaMemcpyAsync(copy, h0, N * state, cudaMemcpyDeviceToDevice, s);
             a.h0 = copy;
         }
-        if (err == cudaSuccess) err = launch_ssm_walk(a, 1, s);
-        if (err == cudaSuccess) err = launch_ssm_walk(a, 2, s);
+        if (err == cudaSuccess) err = walk(a, 1, s);
+        if (err == cudaSuccess) err = walk(a, 2, s);
     } else {
-        err = launch_ssm_walk(a, 0, s);
+        err = walk(a, 0, s);
     }
     if (err == cudaSuccess) return GDR_OK;
     record_cuda_error(err);

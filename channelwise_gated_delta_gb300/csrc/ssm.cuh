@@ -33,4 +33,9 @@ __device__ __forceinline__ float ssm_gate(float y, float z) { return y * (z / (1
 // with their outputs, from the starts that pass 1's states give
 cudaError_t launch_ssm_walk(const SsmArgs &a, int pass, cudaStream_t stream);
 
+// The same on the tensor cores, by chunks of 64 tokens (ssm_tc.cu): bf16, rows
+// that TMA can read.
+bool ssm_chunks_supported(const SsmArgs &a);
+cudaError_t launch_ssm_chunks(const SsmArgs &a, int pass, cudaStream_t stream);
+
 }  // namespace gdr

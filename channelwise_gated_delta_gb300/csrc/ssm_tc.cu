@@ -1,0 +1,895 @@
+// ssm_tc.cu -- gdr_ssm_forward's walk on the tensor cores: bf16 x, b and c,
+// by chunks of 64 tokens, one warp-specialised CTA per (unit of a sequence,
+// value head), the state in registers.
+//
+// With cum the prefix sums of step A within a chunk (kept in log2 units), S
+// the state at its start, r a reference near half of the chunk's decay, all
+// per value head:
+//     M[t][s] = (c_t . b_s) exp(r - cum_s) step_s   (s <= t),  M[t][t] += D exp(r - cum_t)
+//     out^T   = (x^T M^T + (exp(r) S)^T c^T) exp(cum_t - r)
+//     S^T    <- exp(cum_end) S^T + (w x)^T b,   w_s = exp(cum_end - cum_s) step_s
+// so that both parts of an output meet in one accumulator, and M needs no
+// exponential of its own.  That holds while no |cum - r| is above 80 (log2
+// units; a decay of more than 1.7 nats a token).  In a chunk beyond that M
+// takes every pair's own decay, the part from the state is formed first and
+// rescaled in tensor memory, and the rest is added to it.
+//
+// Everything is transposed so that dv fills the 128 rows of an MMA.  Four
+// products a chunk:
+//     G  = c b^T            both tiles as TMA brought them (128-byte swizzle)
+//     Y  = S^T c^T          S^T as bf16 in tensor memory
+//     Y += x^T M^T          x as it came (M-major A), M from the score warps
+//     dS = (w x)^T b        (w x)^T in tensor memory, b as it came
+// x, b and c are exact.  M and w x go in as pairs hi + lo of bf16 numbers, off
+// by 2^-16: the state, which is float32 in registers and never rounded
+// itself, keeps float32's accuracy.  The copy of S that Y reads is rounded
+// once to bf16: its error is averaged over dk products and adds 1 to 27 % to
+// what the output's own rounding leaves (M rounded the same way would add 26
+// to 48 %).
+//
+// The walk's only serial part is S <- g S + dS in the chain warps: dS does not
+// depend on S and is ready ahead, and Y and w x have two buffers each, so that
+// the products follow one another without waiting for the warps.
+//     0-15   chain: lane = value column, 32 of the dk columns each; S in
+//            registers, its bf16 copy into tensor memory
+//     16-19  (w x)^T into tensor memory
+//     20-23  outputs: Y exp(cum - r), times silu(z)
+//     24, 25, 28, 29  scores: rows of G to rows of M (G's 64 rows are TMEM lanes
+//            0-63, which only warps 4 n and 4 n + 1 can read)
+//     26     producer: TMA of x, b, c three chunks ahead, and the chunk's
+//            scalars (steps, prefix sums, decays) two tokens a lane
+//     27, 30 issue the MMAs (one thread each): G and dS; Y.  An MMA takes its
+//            thread as long as the tensor cores (32 to 64 cycles each), and a
+//            thread that waits for one product's inputs feeds no other
+// Every wait is bounded: a timeout sets the CTA's abort flag and the library's
+// error word, and everyone runs out its loop.
+#include <cuda.h>
+#include <limits.h>
+
+#include <type_traits>
+
+#include "gdr.h"
+#include "sm100_ptx.cuh"
+#include "ssm.cuh"
+#include "tma_host.h"
+
+namespace gdr {
+namespace {
+
+using namespace sm100;
+
+constexpr int kC = 64;
+constexpr int kWarps = 31;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kWx0 = 16, kOut0 = 20, kScore0 = 24, kProducer = 26, kIssueState = 27, kIssueY = 30;
+constexpr int kStages = 3;
+constexpr int kRing = 8;  // chunks whose scalars are held
+// a wait's limit: tries of up to kTryNs each, two seconds in all
+constexpr uint32_t kTryNs = 2000;
+constexpr uint32_t kTries = 1u << 20;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// shared memory, from a 1024-byte aligned base
+constexpr uint32_t kTile = 16384;  // 64 rows of up to 128, two boxes of 64 columns
+constexpr uint32_t kX = 0, kB = kTile, kCm = 2 * kTile, kStage = 3 * kTile;
+constexpr uint32_t kM = kStages * kStage;           // [2] x {hi, lo} [64 t][64 s]
+constexpr uint32_t kScal = kM + 2 * 16384;          // [kRing] of the following
+// of a chunk, 64 numbers each: exp(cum - r), w as pairs {hi, lo} of two tokens,
+// exp(r - cum) step, D exp(r - cum); in a chunk beyond r's range kV the sums
+// behind and kCum up to a token within its half, and the steps; then exp(cum_end), exp(r) and whether the chunk is beyond r's range
+constexpr uint32_t kE = 0, kW = 256, kV = 512, kDiag = 768, kCum = 1024, kStep = 1280, kEnd = 1536;
+constexpr uint32_t kScalBytes = 1552;
+constexpr float kRange = 80.f;
+constexpr uint32_t kOut = kScal + kRing * kScalBytes;  // [4 warps] [64 t][32] outputs
+constexpr uint32_t kZ = kOut + 16384;                  // the same of z
+constexpr uint32_t kBars = kZ + 16384;
+enum {
+    FULL = 0,               // [3] x, b, c of a chunk in, and its scalars
+    EMPTY = FULL + kStages,  // [3] its last product done
+    FIX = EMPTY + kStages,   // rows behind the sequence's end zeroed
+    GRAM,                    // G done
+    GFREE,                   // G read
+    MFULL,                   // [2] M written
+    MFREE = MFULL + 2,       // [2] M read
+    WX = MFREE + 2,          // [2] (w x)^T written
+    WFREE = WX + 2,          // [2] (w x)^T read
+    DELTA = WFREE + 2,       // dS done
+    DFREE,                   // dS read
+    SFULL,                   // S copied
+    SFREE,                   // that copy read
+    YDONE,                   // [2] Y done
+    YFREE = YDONE + 2,       // [2] Y read
+    YSCALED = YFREE + 2,     // in a chunk beyond r's range YDONE is the part from the state;
+    YPART,                   // that is rescaled, and the rest added to it
+    LAST,                    // [2] all done
+    kNumBars = LAST + 2
+};
+constexpr uint32_t kSlot = kBars + 8 * kNumBars;
+constexpr uint32_t kAbort = kSlot + 4;
+constexpr uint32_t kSmem = kAbort + 4 + 1024;
+static_assert(kSmem <= 232448 && kOut % 16 == 0 && kBars % 8 == 0, "shared memory");
+
+// tensor memory columns
+constexpr uint32_t kTmG = 0, kTmY = 64, kTmS = 192, kTmD = 256, kTmW = 384, kTmCols = 512;
+
+struct Maps {
+    CUtensorMap x, b, c;
+};
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int c0, int c1,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+// Waits for a phase of the barrier in at most kTries tries of up to kTryNs,
+// or until the CTA's abort flag is set.  One small loop: the kernel's twenty
+// warps run seven different programs out of one instruction cache, and it ran
+// at 0.65 of its speed while their code took 88 KB instead of 60.
+__device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 n, q;\n\t"
+        "mov.b32 n, 0;\n"
+        "TRY_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t"
+        "@p bra DONE_%=;\n\t"
+        "ld.volatile.shared.b32 q, [%5];\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.eq.u32 p, q, 0;\n\t"
+        "setp.lt.and.u32 p, n, %4, p;\n\t"
+        "@p bra TRY_%=;\n"
+        "DONE_%=:\n\t}"
+        : "=&r"(ok)
+        : "r"(bar), "r"(parity), "r"(kTryNs), "r"(kTries), "r"(abort_flag)
+        : "memory");
+    return ok != 0;
+}
+
+// two float32 operations at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// (a, b) as hi + lo, two bf16 numbers each
+__device__ __forceinline__ void pair2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(a, b);
+    const float2 r = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                          make_float2(-1.f, -1.f), make_float2(a, b));
+    lo = pack2(r.x, r.y);
+}
+// x w of two bf16 numbers x and two weights w = wh + wl (bf16 each) as
+// hi + lo: hi = x wh rounded, whose remainder fits eight bits and so bf16,
+// lo = that remainder + x wl.  Off by 2^-17 of hi.
+__device__ __forceinline__ void weigh2(uint32_t x, uint32_t wh, uint32_t wl, uint32_t &hi,
+                                       uint32_t &lo) {
+    asm("{\n\t.reg .b32 n, r;\n\t"
+        "mul.rn.bf16x2 %0, %2, %3;\n\t"
+        "neg.bf16x2 n, %0;\n\t"
+        "fma.rn.bf16x2 r, %2, %3, n;\n\t"
+        "fma.rn.bf16x2 %1, %2, %4, r;\n\t}"
+        : "=&r"(hi), "=r"(lo)
+        : "r"(x), "r"(wh), "r"(wl));
+}
+
+// Four 8 x 8 matrices of 16-bit numbers between shared memory and registers,
+// transposed: a lane's address is that of row lane % 8 of matrix lane / 8, and
+// register i holds rows 2 (lane % 4) and + 1 of column lane / 4 of matrix i.
+__device__ __forceinline__ void ldsm4_t(uint32_t at, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t at, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// Tensor memory in the same arrangement, 16 lanes at a time: 32 columns of
+// float32 (registers 4 j + {0, 1}: lane / 4 of the 16, columns 8 j + 2 (lane %
+// 4) + {0, 1}; + 2: eight lanes on), and 16 columns of pairs (register 2 j:
+// lane / 4, column 4 j + lane % 4; + 1: eight lanes on).
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t at, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_16x128(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+// one lane of a converged warp, the same each time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// silu
+__device__ __forceinline__ float gate(float z) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(-kLog2e * z)));
+    return z * r;
+}
+template <int DK, int PASS>
+__global__ void __launch_bounds__(kThreads, 1)
+    gdr_ssm_chunk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SeqTable table,
+                         const __grid_constant__ Maps maps, int *err) {
+    constexpr bool OUT = PASS != 1;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBars);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem + kSlot);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kAbort);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const int hv = blockIdx.x % a.HV, hk = hv / (a.HV / a.HK);
+    const SeqUnit u = find_unit(table, blockIdx.x / a.HV);
+    const int unit = table.unit0 + blockIdx.x / a.HV;
+    const long long first = (long long)u.unit * a.seg_rows;
+    const int T = (int)min((long long)u.len - first, (long long)a.seg_rows);
+    const bool last = first + T == u.len;
+    if (PASS == 1 && last) return;  // no unit follows
+    const long long row0 = u.row0 + first;
+    const int NC = (T + kC - 1) / kC;
+    const int dv = a.dv;
+    const size_t per = (size_t)DK * dv;
+
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            const int n = i == GFREE || i == MFULL || i == MFULL + 1 || i == WX || i == WX + 1 ||
+                                  i == YFREE || i == YFREE + 1 || i == YSCALED
+                              ? 128
+                          : i == DFREE || i == SFULL               ? 4 * DK
+                          : i >= EMPTY && i < EMPTY + kStages && OUT ? 2
+                                                                     : 1;
+            mbar_init(&bars[i], n);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(slot, kTmCols);
+    // the blocks of M above the diagonal (rows below 32, columns from 32 on) stay zero
+    for (int i = tid; i < 4 * 32 * 4; i += kThreads)
+        *reinterpret_cast<uint4 *>(smem + kM + (i >> 7) * 8192 +
+                                   kmajor_off((i >> 2) & 31, 32 + 8 * (i & 3), kC)) =
+            make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *slot;
+    // A wait that runs out sets the CTA's abort flag; from then on every wait
+    // that is not already over returns, and the loops run out.
+    const uint32_t bar0 = smem_u32(bars), abort0 = smem_u32(smem + kAbort);
+    auto wait = [&](int id, uint32_t parity) {
+        if (!wait_tries(bar0 + 8 * id, parity & 1, abort0)) {
+            if (!*abort_flag && err) atomicExch(err, 1);
+            *abort_flag = 1;
+        }
+    };
+    auto scal = [&](int c, uint32_t what) {
+        return reinterpret_cast<float *>(smem + kScal + (c & (kRing - 1)) * kScalBytes + what);
+    };
+    auto rows_in = [&](int c) { return min(kC, T - c * kC); };
+    // a chunk's stage and the parity of that stage's barriers
+    struct Stage {
+        int st = 0;
+        uint32_t ph = 0;
+        __device__ __forceinline__ void next() {
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+    };
+    Stage at;
+
+    if (warp < DK / 8) {
+        // ================= chain
+        constexpr int NH = 32;
+        const int p = 32 * (warp & 3) + lane, n0 = NH * (warp >> 2);
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const bool on = 32 * (warp & 3) < dv;  // dv is a multiple of 32
+        float dec = 0.f, ref = 0.f;
+        if (NC > 0) {
+            wait(FULL, 0);
+            dec = scal(0, kEnd)[0];
+            ref = scal(0, kEnd)[1];
+        }
+        at.next();
+        mbar_arrive(&bars[DFREE]);
+        float S[NH];
+#pragma unroll
+        for (int i = 0; i < NH; ++i) S[i] = 0.f;
+        if (on && a.h0 && u.unit == 0) {
+            const float *h = a.h0 + ((size_t)u.seq * a.HV + hv) * per + p;
+#pragma unroll
+            for (int i = 0; i < NH; ++i) S[i] = h[(size_t)(n0 + i) * dv];
+        }
+        if (PASS == 2 && on)
+            for (int k = 0; k < u.unit; ++k) {
+                const size_t s = (size_t)(unit - u.unit + k) * a.HV + hv;
+                const float keep = expf(a.seg_log[s]);
+                const float *e = a.seg_state + s * per + p;
+#pragma unroll
+                for (int i = 0; i < NH; ++i) S[i] = fmaf(keep, S[i], e[(size_t)(n0 + i) * dv]);
+            }
+        for (int c = 0; c < NC; ++c, at.next()) {
+            if (OUT) {
+                if (c > 0) wait(SFREE, c - 1);
+                if (on) {
+#pragma unroll
+                    for (int g = 0; g < NH / 16; ++g) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            const float2 q = mul2(make_float2(ref, ref),
+                                                  make_float2(S[16 * g + 2 * m], S[16 * g + 2 * m + 1]));
+                            h[m] = pack2(q.x, q.y);
+                        }
+                        tmem_st8(tl + kTmS + n0 / 2 + 8 * g, h);
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&bars[SFULL]);
+            }
+            const float now = dec;
+            if (c + 1 < NC) {
+                wait(FULL + at.st, at.ph);
+                dec = scal(c + 1, kEnd)[0];
+                ref = scal(c + 1, kEnd)[1];
+            }
+            wait(DELTA, c);
+            tc_fence_after_sync();
+            if (on) {
+                constexpr int W = 16;
+#pragma unroll
+                for (int g = 0; g < NH / W; ++g) {
+                    float d[W];
+                    tmem_ld16(tl + kTmD + n0 + W * g, d);
+#pragma unroll
+                    for (int m = 0; m < W; m += 2) {
+                        const float2 q = fma2(make_float2(now, now),
+                                              make_float2(S[W * g + m], S[W * g + m + 1]),
+                                              make_float2(d[m], d[m + 1]));
+                        S[W * g + m] = q.x;
+                        S[W * g + m + 1] = q.y;
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[DFREE]);
+        }
+        float *end = PASS == 1 ? a.seg_state + ((size_t)unit * a.HV + hv) * per
+                     : a.ht && last ? a.ht + ((size_t)u.seq * a.HV + hv) * per
+                                    : nullptr;
+        if (on && end && !*abort_flag) {
+#pragma unroll
+            for (int i = 0; i < NH; ++i) end[(size_t)(n0 + i) * dv + p] = S[i];
+        }
+    } else if (warp < kWx0) {
+        // no columns for these
+    } else if (warp < kOut0) {
+        // ================= (w x)^T: value columns over the lanes, two tokens a column
+        const int p0 = 32 * (warp & 3);
+        const uint32_t tl = tmem + ((uint32_t)p0 << 16);
+        const bool on = p0 < dv;
+        // this lane's row of the 8 x 8 blocks (tokens 8 j + row, columns p0 + 8 i ..):
+        // matrices 0 and 1 of a load are adjacent columns, 2 and 3 the next tokens
+        const int row = lane & 7;
+        const uint32_t x0 = smem_u32(smem) + kX + (p0 >> 6) * 8192 + ((lane >> 4) * 8 + row) * 128;
+        const int unit = ((p0 & 63) >> 3) + ((lane >> 3) & 1);
+        for (int c = 0; c < NC; ++c, at.next()) {
+            const int st = at.st, L = rows_in(c);
+            wait(FULL + st, at.ph);
+            if (L < kC) wait(FIX, 0);
+            if (c >= 2) wait(WFREE + (c & 1), (c >> 1) - 1);
+            tc_fence_after_sync();
+            if (on) {
+                const uint2 *w = reinterpret_cast<const uint2 *>(scal(c, kW)) + (lane & 3);
+                const uint32_t tw = tl + kTmW + 64 * (c & 1);
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const int hh = k & 1, s32 = k >> 1;  // half of the columns, of the tokens
+                    const uint32_t x = x0 + st * kStage + s32 * 4096 + (((unit + 2 * hh) ^ row) << 4);
+                    uint32_t q[8], h[8], l[8];
+                    ldsm4_t(x, *reinterpret_cast<uint32_t (*)[4]>(q));
+                    ldsm4_t(x + 2048, *reinterpret_cast<uint32_t (*)[4]>(q + 4));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint2 ww = w[16 * s32 + 4 * j];
+                        weigh2(q[2 * j], ww.x, ww.y, h[2 * j], l[2 * j]);
+                        weigh2(q[2 * j + 1], ww.x, ww.y, h[2 * j + 1], l[2 * j + 1]);
+                    }
+                    const uint32_t to = tw + ((uint32_t)(16 * hh) << 16) + 16 * s32;
+                    tmem_st_16x128(to, h);
+                    tmem_st_16x128(to + 32, l);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[WX + (c & 1)]);
+        }
+    } else if (warp < kScore0) {
+        // ================= outputs
+        if (OUT) {
+            const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const bool on = 32 * (warp & 3) < dv;
+            // the warp's 32 columns of a chunk pass through shared memory, so that
+            // they go out (and z comes in) 16 bytes at a time: lane = row
+            // lane / 4 of eight, 16 bytes lane % 4 of it.  There a row's four 16
+            // bytes are XORed with half the row's number, so that eight rows of 8
+            // x 8 blocks fall in different banks.
+            const int r8 = lane >> 2, mine = r8 * 64 + (((lane & 3) ^ ((r8 >> 1) & 3)) << 4);
+            const size_t col = (size_t)hv * dv + 32 * (warp & 3) + 8 * (lane & 3);
+            const size_t ldo = (size_t)a.HV * dv;
+            const uint16_t *z = static_cast<const uint16_t *>(a.z) + (row0 + r8) * a.ldz + col;
+            uint16_t *out = static_cast<uint16_t *>(a.out) + (row0 + r8) * ldo + col;
+            const bool zvec = (((uintptr_t)a.z | (uintptr_t)(a.ldz * 2)) & 15u) == 0;
+            unsigned char *so = smem + kOut + (warp & 3) * 4096, *sz = smem + kZ + (warp & 3) * 4096;
+            const bool gated = a.z != nullptr && on;
+            // this lane's row of the 8 x 8 blocks (tokens, columns) of two loads or stores:
+            // matrices 0 and 1 are adjacent columns, 2 and 3 the next eight tokens
+            const int xr = (lane & 7) >> 1;
+            const uint32_t blk = smem_u32(so) + ((lane >> 4) * 8 + (lane & 7)) * 64;
+            // z of a chunk into shared memory, asynchronously where it is 16-byte aligned
+            auto fetch = [&](int c) {
+                const int L = rows_in(c);
+                const uint16_t *q = z + (long long)c * kC * a.ldz;
+                if (zvec) {
+#pragma unroll 2
+                    for (int k = 0; k < 8; ++k, q += 8 * a.ldz)
+                        if (8 * k + r8 < L) cp_async16(sz + 512 * k + mine, q);
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < 64; ++k) {
+                        const int r = k & 56;  // eight rows at a time, element k & 7
+                        if (r + r8 < L)
+                            *reinterpret_cast<uint16_t *>(sz + 64 * r + mine + 2 * (k & 7)) =
+                                __ldg(q + r * a.ldz + (k & 7));
+                    }
+                }
+            };
+            if (gated && NC > 0) fetch(0);
+            uint32_t beyond = 0;  // chunks beyond r's range so far
+            for (int c = 0; c < NC; ++c) {
+                const int L = rows_in(c);
+                const uint32_t ty = tl + kTmY + 64 * (c & 1);
+                wait(YDONE + (c & 1), c >> 1);
+                tc_fence_after_sync();
+                const float *e = scal(c, kE);
+                if (scal(c, kEnd)[2] != 0.f) {
+                    // that was the part from the state alone: times exp(cum_t)
+                    if (on)
+#pragma unroll 1
+                        for (int g = 0; g < 4; ++g) {
+                            float y[16];
+                            uint32_t q[16];
+                            tmem_ld16(ty + 16 * g, y);
+#pragma unroll
+                            for (int m = 0; m < 16; ++m) q[m] = __float_as_uint(y[m] * e[16 * g + m]);
+                            tmem_st16(ty + 16 * g, q);
+                        }
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    mbar_arrive(&bars[YSCALED]);
+                    wait(YPART, beyond++);
+                    tc_fence_after_sync();
+                    e = scal(c, kDiag);  // ones
+                }
+                auto combine = [&](auto with_z) {
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const int hh = k & 1, t32 = k >> 1;  // half of the columns, of the tokens
+                        const uint32_t at = blk + t32 * 2048 + (((lane >> 3 & 1) + 2 * hh) ^ xr) * 16;
+                        float2 ec[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            ec[j] = *reinterpret_cast<const float2 *>(e + 32 * t32 + 8 * j + 2 * (lane & 3));
+                        uint32_t zt[8];
+                        if (with_z) {
+                            ldsm4_t(at + (kZ - kOut), *reinterpret_cast<uint32_t (*)[4]>(zt));
+                            ldsm4_t(at + (kZ - kOut) + 1024, *reinterpret_cast<uint32_t (*)[4]>(zt + 4));
+                        }
+                        float y[16];
+                        tmem_ld_16x256(ty + ((uint32_t)(16 * hh) << 16) + 32 * t32, y);
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float2 q = mul2(ec[i >> 1], make_float2(y[2 * i], y[2 * i + 1]));
+                            if (with_z) {
+                                q.x *= gate(__uint_as_float(zt[i] << 16));
+                                q.y *= gate(__uint_as_float(zt[i] & 0xffff0000u));
+                            }
+                            o[i] = pack2(q.x, q.y);
+                        }
+                        stsm4_t(at, *reinterpret_cast<const uint32_t (*)[4]>(o));
+                        stsm4_t(at + 1024, *reinterpret_cast<const uint32_t (*)[4]>(o + 4));
+                    }
+                };
+                if (gated) {
+                    cp_async_wait_all();
+                    __syncwarp();
+                    combine(std::true_type{});
+                    __syncwarp();
+                    if (c + 1 < NC) fetch(c + 1);
+                } else if (on)
+                    combine(std::false_type{});
+                tc_fence_before_sync();
+                mbar_arrive(&bars[YFREE + (c & 1)]);
+                if (on) {
+                    __syncwarp();
+                    uint16_t *o = out + (size_t)c * kC * ldo;
+#pragma unroll 4
+                    for (int k = 0; k < 8; ++k, o += 8 * ldo)
+                        if (8 * k + r8 < L)
+                            *reinterpret_cast<uint4 *>(o) =
+                                *reinterpret_cast<const uint4 *>(so + 512 * k + mine);
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp != kProducer && warp != kIssueState && warp != kIssueY) {
+        // ================= scores: lane = token t of the chunk
+        if (OUT) {
+            const int sw = warp & 1, t = 32 * sw + lane;
+            // 16 columns at a time, up to the row's own half; two warps share them
+            const int g0 = ((warp - kScore0) >> 2) << sw;
+            const uint32_t tl = tmem + ((uint32_t)(32 * sw) << 16);
+            const float D = a.D ? a.D[hv] : 0.f;
+            for (int c = 0; c < NC; ++c, at.next()) {
+                const int L = rows_in(c);
+                wait(FULL + at.st, at.ph);
+                wait(GRAM, c);
+                tc_fence_after_sync();
+                if (c >= 2) wait(MFREE + (c & 1), (c >> 1) - 1);
+                unsigned char *m = smem + kM + (c & 1) * 16384 + kmajor_off(t, 0, kC);
+                const bool row = t < L, far = scal(c, kEnd)[2] != 0.f;
+                const float diag = far ? D : scal(c, kDiag)[t], ct = far ? scal(c, kCum)[t] : 0.f;
+#pragma unroll 1
+                for (int g = g0; g < g0 + 1 + sw; ++g) {
+                    float d[16], w[16];
+                    if (!far) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(w + e) =
+                                *reinterpret_cast<const float4 *>(scal(c, kV) + 16 * g + e);
+                    } else {
+                        // exp(cum_t - cum_s) step_s from sums within the halves:
+                        // up to t less up to s, or, across them, plus those behind s
+                        const bool across = 16 * g < 32 * sw;
+                        const float *q = scal(c, across ? kV : kCum) + 16 * g, sign = across ? 1.f : -1.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = fast_exp2(fmaf(sign, q[e], ct)) * scal(c, kStep)[16 * g + e];
+                    }
+                    tmem_ld16(tl + kTmG + 16 * g, d);
+                    const int mine = row ? t - 16 * g : -1;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float q = d[8 * h + e] * w[8 * h + e];
+                            f[e] = 8 * h + e < mine ? q : 8 * h + e == mine ? q + diag : 0.f;
+                        }
+                        uint4 hi, lo;
+                        pair2(f[0], f[1], hi.x, lo.x);
+                        pair2(f[2], f[3], hi.y, lo.y);
+                        pair2(f[4], f[5], hi.z, lo.z);
+                        pair2(f[6], f[7], hi.w, lo.w);
+                        *reinterpret_cast<uint4 *>(m + 128 * (2 * g + h)) = hi;
+                        *reinterpret_cast<uint4 *>(m + 8192 + 128 * (2 * g + h)) = lo;
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&bars[GFREE]);
+                fence_async_smem();
+                mbar_arrive(&bars[MFULL + (c & 1)]);
+            }
+        }
+    } else if (warp == kProducer) {
+        // ================= TMA and scalars: tokens 2 lane and 2 lane + 1
+        const int nx = dv > 64 ? 2 : 1, nb = DK > 64 ? 2 : 1;
+        const float A2 = a.A[hv] * kLog2e, bias = a.dt_bias ? a.dt_bias[hv] : 0.f;
+        const float D = a.D ? a.D[hv] : 0.f;
+        const float *dt = a.dt + row0 * a.HV + hv;
+        auto dt_at = [&](int t) { return t < T ? __ldg(dt + (long long)t * a.HV) : 0.f; };
+        float d0 = dt_at(2 * lane), d1 = dt_at(2 * lane + 1);
+        double total = 0.0;  // log2 of the unit's decay
+        int armed = -1;
+        for (int c = 0; c < NC; ++c, at.next()) {
+            const int st = at.st, t0 = c * kC, t = t0 + 2 * lane;
+            float s0 = ssm_step(d0, bias, a.softplus), s1 = ssm_step(d1, bias, a.softplus);
+            s0 = t < T ? s0 : 0.f;
+            s1 = t + 1 < T ? s1 : 0.f;
+            d0 = dt_at(t + kC);
+            d1 = dt_at(t + kC + 1);
+            const float l0 = s0 * A2, l1 = s1 * A2;
+            // sums within the half chunk of 16 lanes, of the tokens up to each
+            // and of those behind it: no difference of long sums
+            float up = l0 + l1, down = up;
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) {
+                const float o = __shfl_up_sync(0xffffffffu, up, off, 16);
+                const float q = __shfl_down_sync(0xffffffffu, down, off, 16);
+                if ((lane & 15) >= off) up += o;
+                if ((lane & 15) + off < 16) down += q;
+            }
+            float c0 = __shfl_up_sync(0xffffffffu, up, 1, 16);
+            float f1 = __shfl_down_sync(0xffffffffu, down, 1, 16);
+            c0 = ((lane & 15) ? c0 : 0.f) + l0;
+            f1 = (lane & 15) < 15 ? f1 : 0.f;
+            const float c1 = c0 + l1, f0 = f1 + l1;
+            const float all0 = __shfl_sync(0xffffffffu, c1, 15), all1 = __shfl_sync(0xffffffffu, c1, 31);
+            if (PASS == 1) total += (double)all0 + all1;
+            if (c >= kStages) wait(EMPTY + st, at.ph ^ 1);
+            if (*abort_flag) break;
+            float *q = scal(c, 0) + 2 * lane;
+            auto put = [&](uint32_t what, float x, float y) {
+                *reinterpret_cast<float2 *>(q + what / 4) = make_float2(x, y);
+            };
+            const float before = lane < 16 ? 0.f : all0, behind = lane < 16 ? all1 : 0.f;
+            // r a whole number, so that exp(r) S is S but for its exponent
+            float r = rintf(0.5f * (all0 + all1));
+            const float p0 = before + c0, p1 = before + c1;
+            const bool far = __any_sync(0xffffffffu, fabsf(p0 - r) > kRange || fabsf(p1 - r) > kRange);
+            uint2 w;
+            pair2(fast_exp2(behind + f0) * s0, fast_exp2(behind + f1) * s1, w.x, w.y);
+            *reinterpret_cast<uint2 *>(q + kW / 4) = w;
+            if (!far) {
+                const float v0 = fast_exp2(r - p0), v1 = fast_exp2(r - p1);
+                put(kE, fast_exp2(p0 - r), fast_exp2(p1 - r));
+                put(kV, v0 * s0, v1 * s1);
+                put(kDiag, D * v0, D * v1);
+            } else {
+                // kE rescales the part from the state; M is as it is, without D:
+                // its columns of ones are what the outputs are scaled by
+                r = 0.f;
+                put(kE, fast_exp2(p0), fast_exp2(p1));
+                put(kV, f0, f1);
+                put(kCum, c0, c1);
+                put(kStep, s0, s1);
+                put(kDiag, 1.f, 1.f);
+            }
+            if (lane == 0) {
+                float *end = scal(c, kEnd);
+                end[0] = fast_exp2(all0 + all1);
+                end[1] = fast_exp2(r);
+                end[2] = far ? 1.f : 0.f;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                uint64_t *bar = &bars[FULL + st];
+                unsigned char *to = smem + st * kStage;
+                mbar_arrive_expect_tx(bar, (uint32_t)(nx + (OUT ? 2 : 1) * nb) * 8192u);
+                const int row = (int)(row0 + t0);
+                for (int k = 0; k < nx; ++k)
+                    tma_load_2d(to + kX + 8192 * k, &maps.x, hv * dv + 64 * k, row, bar);
+                for (int k = 0; k < nb; ++k) {
+                    tma_load_2d(to + kB + 8192 * k, &maps.b, hk * DK + 64 * k, row, bar);
+                    if (OUT) tma_load_2d(to + kCm + 8192 * k, &maps.c, hk * DK + 64 * k, row, bar);
+                }
+                armed = c;
+            }
+            __syncwarp();
+            const int L = rows_in(c);
+            if (L < kC) {
+                // the last chunk's rows behind the end hold other sequences'
+                // values: zeros, since 0 times those may not be 0
+                wait(FULL + st, at.ph);
+                for (int k = lane; k < (kC - L) * 16; k += 32) {
+                    const int r = L + k / 16;
+                    const uint32_t o = ((k >> 3) & 1) * 8192 + r * 128 + (k & 7) * 16;
+                    *reinterpret_cast<uint4 *>(smem + st * kStage + kX + o) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(smem + st * kStage + kB + o) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[FIX]);
+            }
+        }
+        if (PASS == 1 && lane == 0) {
+            a.seg_log[(size_t)unit * a.HV + hv] = (float)(total * 0.6931471805599453);
+        }
+        if (*abort_flag && lane == 0)  // copies in flight land before the CTA leaves
+            for (int c = armed < kStages ? 0 : armed - kStages + 1; c <= armed; ++c)
+                mbar_wait_bounded(&bars[FULL + c % kStages], (c / kStages) & 1, kWaitNs);
+    } else if (warp == kIssueState) {
+        // ================= MMA issue: G and dS.  The warp waits as one, one lane issues
+        constexpr uint32_t idG = idesc_bf16(128, kC, false, false, false);
+        constexpr uint32_t idD = idesc_bf16(128, DK, false, true, false);
+        // descriptors of stage 0; the stage, a box of 64 columns and a step's
+        // 16 columns (K-major) or rows (MN-major) are added
+        const uint32_t sb = smem_u32(smem);
+        const uint64_t dB = smem_desc_sw128(sb + kB, 16, 1024), dC = smem_desc_sw128(sb + kCm, 16, 1024);
+        const uint64_t dBt = smem_desc_sw128(sb + kB, 8192, 1024);
+        auto gram = [&](int st) {
+            const uint64_t o = (uint64_t)(st * (kStage >> 4));
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_bf16(tmem + kTmG, dC + o + 512 * (ks >> 2) + 2 * (ks & 3),
+                             dB + o + 512 * (ks >> 2) + 2 * (ks & 3), idG, ks > 0);
+                mma_commit(&bars[GRAM]);
+            }
+            __syncwarp();
+        };
+        if (OUT && NC > 0) {
+            wait(FULL, 0);
+            gram(0);
+        }
+        for (int c = 0; c < NC; ++c) {
+            const int st = at.st;
+            const uint64_t o = (uint64_t)(st * (kStage >> 4));
+            at.next();
+            wait(WX + (c & 1), c >> 1);
+            wait(DFREE, c);
+            if (*abort_flag) break;
+            tc_fence_after_sync();
+            if (elect_one()) {
+                const uint32_t w = tmem + kTmW + 64 * (c & 1);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)  // hi, then lo
+                    mma_bf16_ts(tmem + kTmD, w + 8 * ks, dBt + o + 128 * (ks & 3), idD, ks > 0);
+                mma_commit(&bars[DELTA]);
+                mma_commit(&bars[WFREE + (c & 1)]);
+                mma_commit(&bars[EMPTY + st]);
+            }
+            __syncwarp();
+            if (OUT && c + 1 < NC) {
+                wait(FULL + at.st, at.ph);
+                wait(GFREE, c);
+                tc_fence_after_sync();
+                gram(at.st);
+            }
+        }
+        // every MMA is done before the tensor memory goes
+        if (elect_one()) mma_commit(&bars[LAST]);
+        __syncwarp();
+        mbar_wait_bounded(&bars[LAST], 0, kWaitNs);
+    } else if (OUT) {
+        // ================= MMA issue: Y
+        constexpr uint32_t idY2 = idesc_bf16(128, kC, false, false, false);
+        constexpr uint32_t idY1 = idesc_bf16(128, kC, true, false, false);
+        const uint32_t sb = smem_u32(smem);
+        const uint64_t dC = smem_desc_sw128(sb + kCm, 16, 1024), dXt = smem_desc_sw128(sb + kX, 8192, 1024);
+        const uint64_t dM = smem_desc(sb + kM, 128, kC * 16);
+        uint32_t beyond = 0;
+        for (int c = 0; c < NC; ++c, at.next()) {
+            const uint64_t o = (uint64_t)(at.st * (kStage >> 4)), m = dM + (uint64_t)((c & 1) * 1024);
+            const uint32_t y = tmem + kTmY + 64 * (c & 1);
+            wait(FULL + at.st, at.ph);
+            wait(SFULL, c);
+            if (c >= 2) wait(YFREE + (c & 1), (c >> 1) - 1);
+            if (*abort_flag) break;
+            const bool far = scal(c, kEnd)[2] != 0.f;
+            tc_fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_bf16_ts(y, tmem + kTmS + 8 * ks, dC + o + 512 * (ks >> 2) + 2 * (ks & 3), idY2,
+                                ks > 0);
+                mma_commit(&bars[SFREE]);
+                if (far) mma_commit(&bars[YDONE + (c & 1)]);
+            }
+            __syncwarp();
+            if (far) wait(YSCALED, beyond++);
+            wait(MFULL + (c & 1), c >> 1);
+            tc_fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)  // hi, then lo
+                    mma_bf16(y, dXt + o + 128 * (ks & 3), m + 512 * (ks >> 2) + 16 * (ks & 3), idY1, 1);
+                mma_commit(&bars[MFREE + (c & 1)]);
+                mma_commit(far ? &bars[YPART] : &bars[YDONE + (c & 1)]);
+                mma_commit(&bars[EMPTY + at.st]);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(&bars[LAST + 1]);
+        __syncwarp();
+        mbar_wait_bounded(&bars[LAST + 1], 0, kWaitNs);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0) tmem_dealloc(tmem, kTmCols);
+}
+
+// x, b or c as [rows][width], rows ld elements apart: boxes of 64 rows of 64
+bool encode(EncodeTiledFn fn, CUtensorMap *m, const void *p, long long width, long long rows,
+            long long ld) {
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int PASS>
+cudaError_t launch(const SsmArgs &a, const Maps &maps, int *err, cudaStream_t stream) {
+    auto k = gdr_ssm_chunk_kernel<DK, PASS>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    return for_sequences(a.cu, a.N, a.T, a.seg_rows, [&](const SeqTable &t, long long units) {
+        trace_begin(kKernSsm, stream);
+        k<<<(unsigned)(units * a.HV), kThreads, kSmem, stream>>>(a, t, maps, err);
+        trace_end(kKernSsm, stream);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace
+
+bool ssm_chunks_supported(const SsmArgs &a) {
+    const long long rows = a.cu ? a.cu[a.N] : (long long)a.N * a.T;
+    const uintptr_t any = (uintptr_t)a.x | (uintptr_t)a.b | (uintptr_t)a.c;
+    return a.bf16 && rows <= INT_MAX - kC && (any & 15u) == 0 && a.ldx % 8 == 0 && a.ldb % 8 == 0 &&
+           a.ldc % 8 == 0 && a.ldx < (1LL << 38) && a.ldb < (1LL << 38) && a.ldc < (1LL << 38);
+}
+
+cudaError_t launch_ssm_chunks(const SsmArgs &a, int pass, cudaStream_t stream) {
+    int *err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    const EncodeTiledFn fn = tma_encode_fn(&e);
+    if (e != cudaSuccess) return e;
+    const long long rows = a.cu ? a.cu[a.N] : (long long)a.N * a.T;
+    Maps m;
+    if (!encode(fn, &m.x, a.x, (long long)a.HV * a.dv, rows, a.ldx) ||
+        !encode(fn, &m.b, a.b, (long long)a.HK * a.dk, rows, a.ldb) ||
+        !encode(fn, &m.c, a.c, (long long)a.HK * a.dk, rows, a.ldc))
+        return cudaErrorInvalidValue;
+    switch (a.dk) {
+        case 32: return pass == 0 ? launch<32, 0>(a, m, err, stream)
+                        : pass == 1 ? launch<32, 1>(a, m, err, stream) : launch<32, 2>(a, m, err, stream);
+        case 64: return pass == 0 ? launch<64, 0>(a, m, err, stream)
+                        : pass == 1 ? launch<64, 1>(a, m, err, stream) : launch<64, 2>(a, m, err, stream);
+        default: return pass == 0 ? launch<128, 0>(a, m, err, stream)
+                        : pass == 1 ? launch<128, 1>(a, m, err, stream) : launch<128, 2>(a, m, err, stream);
+    }
+}
+
+}  // namespace gdr

@@ -55,11 +55,12 @@ def qk_norm(x, weight=None, scale=1.0, rms=False, eps=1e-6, positions=None, inv_
     return y, err
 
 
-def ssm(x, b, c, dt, a, d=None, z=None, dt_bias=None, h0=None, softplus=True, unit=8 * U):
+def ssm(x, b, c, dt, a, d=None, z=None, dt_bias=None, h0=None, softplus=True, unit=8 * U, read=0.0):
     """x, z [T, HV, dv], b, c [T, HK, dk], dt [T, HV] -> (out, S, error of out, error of S).
 
     ``unit``: the relative error of a state's update, of its decay (beside that of the exponent,
-    which grows with its size) and of what is read out of it."""
+    which grows with its size) and of what is read out of it; ``read``: how far the copy of the
+    state that an output is read from is off, relative to each element."""
     T, HV, dv = x.shape
     HK, dk = b.shape[1:]
     S = np.zeros((HV, dk, dv)) if h0 is None else h0.copy()
@@ -77,7 +78,7 @@ def ssm(x, b, c, dt, a, d=None, z=None, dt_bias=None, h0=None, softplus=True, un
         S = keep * S + new
         size = keep * size + np.abs(new)
         out[t] = (ct * S).sum(1)
-        err[t] = (np.abs(ct) * E).sum(1) + (dk * U + unit) * (np.abs(ct) * size).sum(1)
+        err[t] = (np.abs(ct) * E).sum(1) + (dk * U + unit + read) * (np.abs(ct) * size).sum(1)
         if d is not None:
             out[t] += d[:, None] * x[t]
             err[t] += 2 * U * np.abs(out[t]) + 2 * U * np.abs(d[:, None] * x[t])
