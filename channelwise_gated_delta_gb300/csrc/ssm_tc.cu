@@ -81,9 +81,8 @@ constexpr uint32_t kScal = kM + 2 * 16384;          // [kRing] of the following
 constexpr uint32_t kE = 0, kW = 256, kV = 512, kDiag = 768, kCum = 1024, kStep = 1280, kEnd = 1536;
 constexpr uint32_t kScalBytes = 1552;
 constexpr float kRange = 80.f;
-constexpr uint32_t kOut = kScal + kRing * kScalBytes;  // [4 warps] [64 t][32] outputs
-constexpr uint32_t kZ = kOut + 16384;                  // the same of z
-constexpr uint32_t kBars = kZ + 16384;
+constexpr uint32_t kOut = kScal + kRing * kScalBytes;  // [2][4 warps] [64 t][32] z, then outputs
+constexpr uint32_t kBars = kOut + 2 * 16384;
 enum {
     FULL = 0,               // [3] x, b, c of a chunk in, and its scalars
     EMPTY = FULL + kStages,  // [3] its last product done
@@ -233,6 +232,33 @@ __device__ __forceinline__ void tmem_st_16x128(uint32_t at, const uint32_t (&r)[
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_wait_but_one() {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+// `steps` products of 16 along K, the operands' descriptors (of which only the
+// address, in the low half, moves) in steps of their own; one of A's is
+// tensor memory where TS.  A step that ends a box of 64 columns moves by
+// `jump` more.
+template <bool TS>
+__device__ __forceinline__ void products(uint32_t d, uint64_t a, int a_step, int a_jump, uint64_t b,
+                                         int b_step, int b_jump, uint32_t idesc, int steps,
+                                         uint32_t accumulate) {
+    uint32_t al = (uint32_t)a, bl = (uint32_t)b;
+    const uint64_t ah = a & 0xffffffff00000000ull, bh = b & 0xffffffff00000000ull;
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+        if (TS)
+            mma_bf16_ts(d, al, bh | bl, idesc, accumulate);
+        else
+            mma_bf16(d, ah | al, bh | bl, idesc, accumulate);
+        accumulate = 1;
+        al += (uint32_t)(a_step + (k == 3 ? a_jump : 0));
+        bl += (uint32_t)(b_step + (k == 3 ? b_jump : 0));
+    }
+}
 // one lane of a converged warp, the same each time
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -287,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) tmem_alloc(slot, kTmCols);
     // the blocks of M above the diagonal (rows below 32, columns from 32 on) stay zero
+#pragma unroll 1
     for (int i = tid; i < 4 * 32 * 4; i += kThreads)
         *reinterpret_cast<uint4 *>(smem + kM + (i >> 7) * 8192 +
                                    kmajor_off((i >> 2) & 31, 32 + 8 * (i & 3), kC)) =
@@ -340,17 +367,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NH; ++i) S[i] = 0.f;
         if (on && a.h0 && u.unit == 0) {
-            const float *h = a.h0 + ((size_t)u.seq * a.HV + hv) * per + p;
+            const float *h = a.h0 + ((size_t)u.seq * a.HV + hv) * per + n0 * dv + p;
 #pragma unroll
-            for (int i = 0; i < NH; ++i) S[i] = h[(size_t)(n0 + i) * dv];
+            for (int i = 0; i < NH; ++i, h += dv) S[i] = *h;
         }
         if (PASS == 2 && on)
+#pragma unroll 1
             for (int k = 0; k < u.unit; ++k) {
                 const size_t s = (size_t)(unit - u.unit + k) * a.HV + hv;
                 const float keep = expf(a.seg_log[s]);
-                const float *e = a.seg_state + s * per + p;
+                const float *e = a.seg_state + s * per + n0 * dv + p;
 #pragma unroll
-                for (int i = 0; i < NH; ++i) S[i] = fmaf(keep, S[i], e[(size_t)(n0 + i) * dv]);
+                for (int i = 0; i < NH; ++i, e += dv) S[i] = fmaf(keep, S[i], *e);
             }
         for (int c = 0; c < NC; ++c, at.next()) {
             if (OUT) {
@@ -403,8 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : a.ht && last ? a.ht + ((size_t)u.seq * a.HV + hv) * per
                                     : nullptr;
         if (on && end && !*abort_flag) {
+            end += n0 * dv + p;
 #pragma unroll
-            for (int i = 0; i < NH; ++i) end[(size_t)(n0 + i) * dv + p] = S[i];
+            for (int i = 0; i < NH; ++i, end += dv) *end = S[i];
         }
     } else if (warp < kWx0) {
         // no columns for these
@@ -465,35 +494,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint16_t *z = static_cast<const uint16_t *>(a.z) + (row0 + r8) * a.ldz + col;
             uint16_t *out = static_cast<uint16_t *>(a.out) + (row0 + r8) * ldo + col;
             const bool zvec = (((uintptr_t)a.z | (uintptr_t)(a.ldz * 2)) & 15u) == 0;
-            unsigned char *so = smem + kOut + (warp & 3) * 4096, *sz = smem + kZ + (warp & 3) * 4096;
+            unsigned char *so = smem + kOut + (warp & 3) * 4096;
             const bool gated = a.z != nullptr && on;
             // this lane's row of the 8 x 8 blocks (tokens, columns) of two loads or stores:
             // matrices 0 and 1 are adjacent columns, 2 and 3 the next eight tokens
             const int xr = (lane & 7) >> 1;
             const uint32_t blk = smem_u32(so) + ((lane >> 4) * 8 + (lane & 7)) * 64;
-            // z of a chunk into shared memory, asynchronously where it is 16-byte aligned
+            // z of a chunk into shared memory, asynchronously where it is 16-byte
+            // aligned; the outputs take its place
             auto fetch = [&](int c) {
                 const int L = rows_in(c);
                 const uint16_t *q = z + (long long)c * kC * a.ldz;
+                unsigned char *sz = so + (c & 1) * 16384 + mine;
                 if (zvec) {
 #pragma unroll 2
                     for (int k = 0; k < 8; ++k, q += 8 * a.ldz)
-                        if (8 * k + r8 < L) cp_async16(sz + 512 * k + mine, q);
+                        if (8 * k + r8 < L) cp_async16(sz + 512 * k, q);
                 } else {
 #pragma unroll 1
                     for (int k = 0; k < 64; ++k) {
                         const int r = k & 56;  // eight rows at a time, element k & 7
                         if (r + r8 < L)
-                            *reinterpret_cast<uint16_t *>(sz + 64 * r + mine + 2 * (k & 7)) =
+                            *reinterpret_cast<uint16_t *>(sz + 64 * r + 2 * (k & 7)) =
                                 __ldg(q + r * a.ldz + (k & 7));
                     }
                 }
+                cp_async_commit();
             };
             if (gated && NC > 0) fetch(0);
             uint32_t beyond = 0;  // chunks beyond r's range so far
             for (int c = 0; c < NC; ++c) {
                 const int L = rows_in(c);
                 const uint32_t ty = tl + kTmY + 64 * (c & 1);
+                if (gated) {
+                    if (c + 1 < NC)
+                        fetch(c + 1);
+                    else
+                        cp_async_commit();
+                }
                 wait(YDONE + (c & 1), c >> 1);
                 tc_fence_after_sync();
                 const float *e = scal(c, kE);
@@ -520,15 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         const int hh = k & 1, t32 = k >> 1;  // half of the columns, of the tokens
-                        const uint32_t at = blk + t32 * 2048 + (((lane >> 3 & 1) + 2 * hh) ^ xr) * 16;
+                        const uint32_t at = blk + (c & 1) * 16384 + t32 * 2048 + (((lane >> 3 & 1) + 2 * hh) ^ xr) * 16;
                         float2 ec[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             ec[j] = *reinterpret_cast<const float2 *>(e + 32 * t32 + 8 * j + 2 * (lane & 3));
                         uint32_t zt[8];
                         if (with_z) {
-                            ldsm4_t(at + (kZ - kOut), *reinterpret_cast<uint32_t (*)[4]>(zt));
-                            ldsm4_t(at + (kZ - kOut) + 1024, *reinterpret_cast<uint32_t (*)[4]>(zt + 4));
+                            ldsm4_t(at, *reinterpret_cast<uint32_t (*)[4]>(zt));
+                            ldsm4_t(at + 1024, *reinterpret_cast<uint32_t (*)[4]>(zt + 4));
                         }
                         float y[16];
                         tmem_ld_16x256(ty + ((uint32_t)(16 * hh) << 16) + 32 * t32, y);
@@ -547,11 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if (gated) {
-                    cp_async_wait_all();
+                    cp_async_wait_but_one();
                     __syncwarp();
                     combine(std::true_type{});
-                    __syncwarp();
-                    if (c + 1 < NC) fetch(c + 1);
                 } else if (on)
                     combine(std::false_type{});
                 tc_fence_before_sync();
@@ -559,11 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (on) {
                     __syncwarp();
                     uint16_t *o = out + (size_t)c * kC * ldo;
-#pragma unroll 4
+#pragma unroll 2
                     for (int k = 0; k < 8; ++k, o += 8 * ldo)
                         if (8 * k + r8 < L)
                             *reinterpret_cast<uint4 *>(o) =
-                                *reinterpret_cast<const uint4 *>(so + 512 * k + mine);
+                                *reinterpret_cast<const uint4 *>(so + (c & 1) * 16384 + 512 * k + mine);
                     __syncwarp();
                 }
             }
@@ -572,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= scores: lane = token t of the chunk
         if (OUT) {
             const int sw = warp & 1, t = 32 * sw + lane;
-            // 16 columns at a time, up to the row's own half; two warps share them
+            // two warps share the columns up to the row's own half: the first half's rows
+            // take 16 each, the second's 32
             const int g0 = ((warp - kScore0) >> 2) << sw;
             const uint32_t tl = tmem + ((uint32_t)(32 * sw) << 16);
             const float D = a.D ? a.D[hv] : 0.f;
@@ -703,8 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unsigned char *to = smem + st * kStage;
                 mbar_arrive_expect_tx(bar, (uint32_t)(nx + (OUT ? 2 : 1) * nb) * 8192u);
                 const int row = (int)(row0 + t0);
+#pragma unroll 1
                 for (int k = 0; k < nx; ++k)
                     tma_load_2d(to + kX + 8192 * k, &maps.x, hv * dv + 64 * k, row, bar);
+#pragma unroll 1
                 for (int k = 0; k < nb; ++k) {
                     tma_load_2d(to + kB + 8192 * k, &maps.b, hk * DK + 64 * k, row, bar);
                     if (OUT) tma_load_2d(to + kCm + 8192 * k, &maps.c, hk * DK + 64 * k, row, bar);
@@ -717,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the last chunk's rows behind the end hold other sequences'
                 // values: zeros, since 0 times those may not be 0
                 wait(FULL + st, at.ph);
+#pragma unroll 1
                 for (int k = lane; k < (kC - L) * 16; k += 32) {
                     const int r = L + k / 16;
                     const uint32_t o = ((k >> 3) & 1) * 8192 + r * 128 + (k & 7) * 16;
@@ -732,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.seg_log[(size_t)unit * a.HV + hv] = (float)(total * 0.6931471805599453);
         }
         if (*abort_flag && lane == 0)  // copies in flight land before the CTA leaves
+#pragma unroll 1
             for (int c = armed < kStages ? 0 : armed - kStages + 1; c <= armed; ++c)
                 mbar_wait_bounded(&bars[FULL + c % kStages], (c / kStages) & 1, kWaitNs);
     } else if (warp == kIssueState) {
@@ -746,10 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto gram = [&](int st) {
             const uint64_t o = (uint64_t)(st * (kStage >> 4));
             if (elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16(tmem + kTmG, dC + o + 512 * (ks >> 2) + 2 * (ks & 3),
-                             dB + o + 512 * (ks >> 2) + 2 * (ks & 3), idG, ks > 0);
+                products<false>(tmem + kTmG, dC + o, 2, 504, dB + o, 2, 504, idG, DK / 16, 0);
                 mma_commit(&bars[GRAM]);
             }
             __syncwarp();
@@ -767,10 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (*abort_flag) break;
             tc_fence_after_sync();
             if (elect_one()) {
-                const uint32_t w = tmem + kTmW + 64 * (c & 1);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)  // hi, then lo
-                    mma_bf16_ts(tmem + kTmD, w + 8 * ks, dBt + o + 128 * (ks & 3), idD, ks > 0);
+                // hi, then lo, against the same rows
+                products<true>(tmem + kTmD, tmem + kTmW + 64 * (c & 1), 8, 0, dBt + o, 128, -512, idD, 8, 0);
                 mma_commit(&bars[DELTA]);
                 mma_commit(&bars[WFREE + (c & 1)]);
                 mma_commit(&bars[EMPTY + st]);
@@ -805,10 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool far = scal(c, kEnd)[2] != 0.f;
             tc_fence_after_sync();
             if (elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16_ts(y, tmem + kTmS + 8 * ks, dC + o + 512 * (ks >> 2) + 2 * (ks & 3), idY2,
-                                ks > 0);
+                products<true>(y, tmem + kTmS, 8, 0, dC + o, 2, 504, idY2, DK / 16, 0);
                 mma_commit(&bars[SFREE]);
                 if (far) mma_commit(&bars[YDONE + (c & 1)]);
             }
@@ -817,9 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(MFULL + (c & 1), c >> 1);
             tc_fence_after_sync();
             if (elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)  // hi, then lo
-                    mma_bf16(y, dXt + o + 128 * (ks & 3), m + 512 * (ks >> 2) + 16 * (ks & 3), idY1, 1);
+                // M's hi, then its lo (8192 bytes on), against the same x
+                products<false>(y, dXt + o, 128, -512, m, 16, 448, idY1, 8, 1);
                 mma_commit(&bars[MFREE + (c & 1)]);
                 mma_commit(far ? &bars[YPART] : &bars[YDONE + (c & 1)]);
                 mma_commit(&bars[EMPTY + at.st]);
