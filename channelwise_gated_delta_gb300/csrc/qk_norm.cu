@@ -13,43 +13,18 @@
 // heads that it walks.
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "gdr.h"
 #include "packed.cuh"
+#include "sm100_ptx.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kWarps = 4;
-
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-}
+constexpr int kBatch = 4;  // groups of heads whose loads are in flight together
 
 struct NormArgs {
     const void *q, *k;
@@ -63,82 +38,166 @@ struct NormArgs {
     float eps, q_scale, inv_n;
 };
 
-// ROT: 0 none, 1 channel i with i + d_rot / 2, 2 channel 2 i with 2 i + 1.
+// ROT: 0 none, 1 channel i with i + d_rot / 2, 2 channel 2 i with 2 i + 1,
+// 3 as 1 with d_rot = d.  A lane holds 8 adjacent channels; in 3 it holds four
+// and the four half a head on, so that pairs are its own.
+template <typename T, int D, int ROT>
+struct Lane {
+    static constexpr int kSplit = ROT == 3 ? D / 2 : 4;
+    static __device__ __forceinline__ int first(int l) { return ROT == 3 ? 4 * l : 8 * l; }
+    using Raw = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
+    Raw a, b;
+    __device__ __forceinline__ void load(const T *p) {
+        a = *reinterpret_cast<const Raw *>(p);
+        b = *reinterpret_cast<const Raw *>(p + kSplit);
+    }
+    __device__ __forceinline__ void zero() { a = b = Raw{}; }
+    static __device__ __forceinline__ void unpack4(uint2 r, float *f) {
+        f[0] = __uint_as_float(r.x << 16);
+        f[1] = __uint_as_float(r.x & 0xffff0000u);
+        f[2] = __uint_as_float(r.y << 16);
+        f[3] = __uint_as_float(r.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void unpack4(float4 r, float *f) {
+        f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+    }
+    static __device__ __forceinline__ void pack4(const float *f, uint2 *r) {
+        __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
+        *r = make_uint2(*reinterpret_cast<uint32_t *>(&x), *reinterpret_cast<uint32_t *>(&y));
+    }
+    static __device__ __forceinline__ void pack4(const float *f, float4 *r) {
+        *r = make_float4(f[0], f[1], f[2], f[3]);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        unpack4(a, f);
+        unpack4(b, f + 4);
+    }
+    static __device__ __forceinline__ void store(T *p, const float (&f)[8]) {
+        Raw x, y;
+        pack4(f, &x);
+        pack4(f + 4, &y);
+        *reinterpret_cast<Raw *>(p) = x;
+        *reinterpret_cast<Raw *>(p + kSplit) = y;
+    }
+};
+
+// sine and cosine of t half turns, |t| <= 1: for bf16 outputs by the special
+// function unit (off by 2^-21)
+template <typename T>
+__device__ __forceinline__ void turn(float t, float *sn, float *cs) {
+    if (sizeof(T) == 2)
+        __sincosf(t * 3.14159265358979f, sn, cs);
+    else
+        sincospif(t, sn, cs);
+}
+
 template <typename T, int D, int ROT>
 __global__ void __launch_bounds__(32 * kWarps) gdr_qk_norm_kernel(const NormArgs a) {
+    using V = Lane<T, D, ROT>;
     constexpr int L = D / 8, G = 32 / L;  // lanes of a head, heads of a warp's step
     const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
     const long long w = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
     const long long row = w / a.parts;
     if (row >= a.rows) return;
-    const int c = 8 * l;
+    const int c = V::first(l);
 
-    float cs[8], sn[8];  // of the channel's pair; interleaved: of pair i / 2
+    constexpr int P = ROT == 1 ? 8 : 4;  // pairs that this lane needs
+    float cs[P], sn[P];
     const int half = a.d_rot / 2;
-    const bool turned = ROT && c < a.d_rot, upper = ROT == 1 && c >= half;
+    const bool turned = ROT == 3 || (ROT && c < a.d_rot), upper = ROT == 1 && c >= half;
     if (ROT && turned) {
         const long long p = a.pos[row];
 #pragma unroll
-        for (int e = 0; e < (ROT == 1 ? 8 : 4); ++e) {
-            const int i = ROT == 1 ? (upper ? c - half : c) + e : c / 2 + e;
-            const unsigned long long turn = (unsigned long long)p * __ldg(a.freq + i);
+        for (int e = 0; e < P; ++e) {
+            const int i = ROT == 1 ? (upper ? c - half : c) + e : ROT == 2 ? c / 2 + e : c + e;
+            const unsigned long long turns = (unsigned long long)p * __ldg(a.freq + i);
             // the nearest 2^-32 of a turn, in half turns within [-1, 1)
-            const int t = (int)(unsigned)((turn + 0x80000000ull) >> 32);
-            sincospif((float)t * 0x1p-31f, &sn[e], &cs[e]);
+            const int t = (int)(unsigned)((turns + 0x80000000ull) >> 32);
+            turn<T>((float)t * 0x1p-31f, &sn[e], &cs[e]);
+            if (ROT == 1 && !upper) sn[e] = -sn[e];
         }
     }
     const int from = upper ? l - half / 8 : l + half / 8;
-    const int partner = sub * L + (turned ? from : l);
+    const int partner = sub * L + (ROT == 1 && turned ? from : l);
 
+    // the warp's groups of heads: some of q, then some of k
     const int nq = (a.HQ + G - 1) / G, nk = (a.HK + G - 1) / G;
     const int g0 = (int)(w % a.parts) * a.per_warp, g1 = min(g0 + a.per_warp, nq + nk);
-    for (int g = g0; g < g1; ++g) {
-        const bool is_q = g < nq;
-        const int head = (is_q ? g : g - nq) * G + sub;
-        const bool on = head < (is_q ? a.HQ : a.HK);
-        float x[8];
-        if (on) {
-            const T *src = is_q ? static_cast<const T *>(a.q) + row * a.ldq
-                                : static_cast<const T *>(a.k) + row * a.ldk;
-            load8(src + head * D + c, x);
-        } else {
+    auto walk = [&](const T *src, T *dst, const float *weight, int heads, float scale, int first,
+                    int last) {
+        if (first >= last) return;
+        float wt[8];
+        if (weight) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            for (int e = 0; e < 8; ++e) wt[e] = __ldg(weight + c + (e < 4 ? e : V::kSplit + e - 4));
         }
-        float s = 0.f;
+        src += c;
+        dst += c;
+        for (int g = first; g < last; g += kBatch) {
+            V v[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
-#pragma unroll
-        for (int off = L / 2; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s = fmaf(s, a.inv_n, a.eps);
-        // a head of zeros without eps stays zeros
-        const float inv = s == 0.f ? 0.f : (is_q ? a.q_scale : 1.f) / sqrtf(s);
-        const float *wt = is_q ? a.wq : a.wk;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] *= inv;
-            if (wt) x[e] *= __ldg(wt + c + e);
-        }
-        if (ROT == 1) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = __shfl_sync(0xffffffffu, x[e], partner);
-                if (turned) x[e] = upper ? fmaf(x[e], cs[e], y * sn[e]) : fmaf(x[e], cs[e], -y * sn[e]);
+            for (int k = 0; k < kBatch; ++k) {
+                const int head = (g + k) * G + sub;
+                if (g + k < last && head < heads)
+                    v[k].load(src + head * D);
+                else
+                    v[k].zero();
             }
-        } else if (ROT == 2 && turned) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float p = x[2 * e], q = x[2 * e + 1];
-                x[2 * e] = fmaf(p, cs[e], -q * sn[e]);
-                x[2 * e + 1] = fmaf(q, cs[e], p * sn[e]);
+            for (int k = 0; k < kBatch; ++k) {
+                if (g + k >= last) break;
+                const int head = (g + k) * G + sub;
+                float x[8];
+                v[k].unpack(x);
+                float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 y = make_float2(x[e], x[e + 1]);
+                    q = sm100::fma2(y, y, q);
+                }
+                float s = q.x + q.y;
+#pragma unroll
+                for (int off = L / 2; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+                s = fmaf(s, a.inv_n, a.eps);
+                // the approximate root, one step nearer; a head of zeros without
+                // eps stays zeros, one whose sum is infinite becomes zeros
+                float r = rsqrtf(s);
+                r = fmaf(0.5f * r, fmaf(-s * r, r, 1.f), r);
+                const float inv = s == 0.f || s == INFINITY ? 0.f : scale * r;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] *= inv;
+                    if (weight) x[e] *= wt[e];
+                }
+                if (ROT == 1) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = __shfl_sync(0xffffffffu, x[e], partner);
+                        if (turned) x[e] = fmaf(x[e], cs[e % P], y * sn[e % P]);
+                    }
+                } else if (ROT == 2 && turned) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = x[2 * e], y = x[2 * e + 1];
+                        x[2 * e] = fmaf(p, cs[e], -y * sn[e]);
+                        x[2 * e + 1] = fmaf(y, cs[e], p * sn[e]);
+                    }
+                } else if (ROT == 3) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = x[e], y = x[4 + e];
+                        x[e] = fmaf(p, cs[e], -y * sn[e]);
+                        x[4 + e] = fmaf(y, cs[e], p * sn[e]);
+                    }
+                }
+                if (head < heads) V::store(dst + head * D, x);
             }
         }
-        if (on) {
-            T *dst = is_q ? static_cast<T *>(a.oq) + row * a.ldoq
-                          : static_cast<T *>(a.ok) + row * a.ldok;
-            store8(dst + head * D + c, x);
-        }
-    }
+    };
+    walk(static_cast<const T *>(a.q) + row * a.ldq, static_cast<T *>(a.oq) + row * a.ldoq, a.wq, a.HQ,
+         a.q_scale, g0, min(g1, nq));
+    walk(static_cast<const T *>(a.k) + row * a.ldk, static_cast<T *>(a.ok) + row * a.ldok, a.wk, a.HK,
+         1.f, max(g0 - nq, 0), g1 - nq);
 }
 
 template <typename T, int D, int ROT>
@@ -162,6 +221,7 @@ cudaError_t launch(NormArgs a, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t by_rotation(const NormArgs &a, bool interleaved, cudaStream_t s) {
     if (a.d_rot == 0) return launch<T, D, 0>(a, s);
+    if (!interleaved && a.d_rot == D) return launch<T, D, 3>(a, s);
     return interleaved ? launch<T, D, 2>(a, s) : launch<T, D, 1>(a, s);
 }
 

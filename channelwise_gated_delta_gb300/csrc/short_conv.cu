@@ -36,26 +36,19 @@ struct Vec<float, 4> {
     static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
 };
 template <>
-struct Vec<__nv_bfloat16, 8> {
-    using Raw = uint4;
-    static __device__ __forceinline__ void unpack(Raw r, float (&f)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+struct Vec<__nv_bfloat16, 4> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(Raw r, float (&f)[4]) {
+        f[0] = __uint_as_float(r.x << 16);
+        f[1] = __uint_as_float(r.x & 0xffff0000u);
+        f[2] = __uint_as_float(r.y << 16);
+        f[3] = __uint_as_float(r.y & 0xffff0000u);
     }
-    static __device__ __forceinline__ Raw pack(const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<uint32_t *>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+    static __device__ __forceinline__ Raw pack(const float (&f)[4]) {
+        __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+        return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
     }
-    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+    static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
 };
 template <>
 struct Vec<float, 1> {
@@ -73,14 +66,6 @@ struct Vec<__nv_bfloat16, 1> {
     }
     static __device__ __forceinline__ Raw zero() { return from_f32<__nv_bfloat16>(0.f); }
 };
-
-// y / (1 + e^-y)
-__device__ __forceinline__ float silu(float y) {
-    constexpr float kLog2e = 1.4426950408889634f;
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + sm100::fast_exp2(-kLog2e * y)));
-    return y * r;
-}
 
 template <typename T, int W, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads)
@@ -133,27 +118,50 @@ __global__ void __launch_bounds__(kThreads)
             *reinterpret_cast<Raw *>(st + state + (size_t)i * D) = r;
         }
     }
-    for (int t0 = r0; t0 < r1; t0 += kStep) {
-        Raw in[kStep];
+    // kStep rows at a time, the next ones on their way meanwhile
+    Raw in[kStep];
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) in[k] = t0 + k < r1 ? row(t0 + k) : V::zero();
+    for (int k = 0; k < kStep; ++k) in[k] = r0 + k < r1 ? row(r0 + k) : V::zero();
+    for (int t0 = r0; t0 < r1; t0 += kStep) {
+        Raw next[kStep];
+        const bool whole = t0 + 2 * kStep <= r1;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k)
+            next[k] = whole || t0 + kStep + k < r1 ? row(t0 + kStep + k) : V::zero();
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
             float f[VEC], y[VEC];
             V::unpack(in[k], f);
+            if constexpr (VEC % 2 == 0) {
+#pragma unroll
+                for (int v = 0; v < VEC; v += 2) {
+                    float2 q = make_float2(b[v], b[v + 1]);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j)
+                        q = sm100::fma2(make_float2(tap[j][v], tap[j][v + 1]),
+                                        make_float2(win[j][v], win[j][v + 1]), q);
+                    q = sm100::fma2(make_float2(tap[W - 1][v], tap[W - 1][v + 1]),
+                                    make_float2(f[v], f[v + 1]), q);
+                    y[v] = q.x;
+                    y[v + 1] = q.y;
+                }
+            } else {
+                y[0] = b[0];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) y[0] = fmaf(tap[j][0], win[j][0], y[0]);
+                y[0] = fmaf(tap[W - 1][0], f[0], y[0]);
+            }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                y[v] = b[v];
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) y[v] = fmaf(tap[j][v], win[j][v], y[v]);
-                y[v] = fmaf(tap[W - 1][v], f[v], y[v]);
-                if (SILU) y[v] = silu(y[v]);
+                if (SILU) y[v] = sm100::silu(y[v]);
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
                 win[W - 2][v] = f[v];
             }
             if (t0 + k < r1) *reinterpret_cast<Raw *>(out + (t0 + k) * ldo) = V::pack(y);
         }
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) in[k] = next[k];
     }
 }
 
@@ -218,8 +226,8 @@ extern "C" GDR_API gdr_status gdr_short_conv(const void *x, const float *w, cons
         rows_overlap(o, r1) || rows_overlap(r1, in) || rows_overlap(r1, wr) ||
         rows_overlap(r1, br) || (s0 != st && rows_overlap(r1, r0)))
         return GDR_ERR_ALIAS;
-    const int vec = dtype == GDR_BF16 ? 8 : 4;
-    const bool wide = D % vec == 0 && ldx % vec == 0 && ldo % vec == 0 && (any & 15u) == 0;
+    const int vec = 4;
+    const bool wide = D % vec == 0 && ldx % vec == 0 && ldo % vec == 0 && (any & (vec * es - 1)) == 0;
     // rows of a thread: as many as leave every SM some CTAs, at least W - 1
     const long long ny = (D / (wide ? vec : 1) + kThreads - 1) / kThreads;
     if (ny > 65535) return GDR_ERR_SHAPE;
@@ -231,7 +239,7 @@ extern "C" GDR_API gdr_status gdr_short_conv(const void *x, const float *w, cons
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (dtype == GDR_BF16)
-        e = wide ? by_width<__nv_bfloat16, 8>(a, W, rows, s) : by_width<__nv_bfloat16, 1>(a, W, rows, s);
+        e = wide ? by_width<__nv_bfloat16, 4>(a, W, rows, s) : by_width<__nv_bfloat16, 1>(a, W, rows, s);
     else
         e = wide ? by_width<float, 4>(a, W, rows, s) : by_width<float, 1>(a, W, rows, s);
     if (e == cudaSuccess) return GDR_OK;

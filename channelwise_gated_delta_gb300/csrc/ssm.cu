@@ -153,6 +153,100 @@ __global__ void __launch_bounds__(kThreads)
         for (int r = 0; r < R; ++r) end[at + (size_t)r * a.dv] = S[r];
 }
 
+// Sequences of one token (or none): one CTA per (sequence, value head) passes
+// its state through registers once, 16 bytes a thread and row; a warp's row
+// or rows are adjacent, and all of a thread's loads are in flight together.
+constexpr int kStepWarps = 8;
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(32 * kStepWarps)
+    gdr_ssm_step_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SeqTable table) {
+    constexpr int L = DV / 4, RW = 32 / L;              // lanes of a row, rows of a warp's access
+    constexpr int N = DK / (RW * kStepWarps);           // accesses of a thread
+    __shared__ float sb[DK], sc[DK];
+    __shared__ __align__(16) float part[kStepWarps][DV];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane / L, col = 4 * (lane % L);
+    const int hv = blockIdx.x % a.HV, hk = hv / (a.HV / a.HK);
+    const SeqUnit u = find_unit(table, blockIdx.x / a.HV);
+    const size_t state = ((size_t)u.seq * a.HV + hv) * DK * DV + (size_t)(warp * RW + sub) * DV + col;
+    constexpr int kHop = kStepWarps * RW * DV;
+    float4 S[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        S[i] = a.h0 ? ldg_stream4(a.h0 + state + i * kHop) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float keep = 1.f, step = 0.f;
+    float4 xs = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (u.len > 0) {
+        const T *x = static_cast<const T *>(a.x) + u.row0 * a.ldx + (size_t)hv * DV + col;
+        const float x0 = to_f32(x[0]), x1 = to_f32(x[1]), x2 = to_f32(x[2]), x3 = to_f32(x[3]);
+        const float raw = a.dt[u.row0 * a.HV + hv];
+        if (tid < DK)
+            sb[tid] = to_f32(static_cast<const T *>(a.b)[u.row0 * a.ldb + (size_t)hk * DK + tid]);
+        else if (tid < 2 * DK)
+            sc[tid - DK] = to_f32(static_cast<const T *>(a.c)[u.row0 * a.ldc + (size_t)hk * DK + tid - DK]);
+        step = ssm_step(raw, a.dt_bias ? a.dt_bias[hv] : 0.f, a.softplus);
+        keep = expf(step * a.A[hv]);
+        xs = make_float4(step * x0, step * x1, step * x2, step * x3);
+    } else if (tid < DK) {
+        sb[tid] = sc[tid] = 0.f;
+    }
+    __syncthreads();
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = (i * kStepWarps + warp) * RW + sub;
+        const float b = sb[r], c = sc[r];
+        S[i].x = fmaf(keep, S[i].x, b * xs.x);
+        S[i].y = fmaf(keep, S[i].y, b * xs.y);
+        S[i].z = fmaf(keep, S[i].z, b * xs.z);
+        S[i].w = fmaf(keep, S[i].w, b * xs.w);
+        y.x = fmaf(c, S[i].x, y.x);
+        y.y = fmaf(c, S[i].y, y.y);
+        y.z = fmaf(c, S[i].z, y.z);
+        y.w = fmaf(c, S[i].w, y.w);
+        if (a.ht) stg_stream4(a.ht + state + i * kHop, S[i]);
+    }
+    if (u.len == 0) return;
+#pragma unroll
+    for (int off = L; off < 32; off <<= 1) {
+        y.x += __shfl_xor_sync(0xffffffffu, y.x, off);
+        y.y += __shfl_xor_sync(0xffffffffu, y.y, off);
+        y.z += __shfl_xor_sync(0xffffffffu, y.z, off);
+        y.w += __shfl_xor_sync(0xffffffffu, y.w, off);
+    }
+    if (sub == 0) *reinterpret_cast<float4 *>(&part[warp][col]) = y;
+    __syncthreads();
+    if (tid < DV) {
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kStepWarps; ++w) o += part[w][tid];
+        const size_t at = (size_t)hv * DV + tid;
+        if (a.D) o = fmaf(a.D[hv], to_f32(static_cast<const T *>(a.x)[u.row0 * a.ldx + at]), o);
+        if (a.z) o = ssm_gate(o, to_f32(static_cast<const T *>(a.z)[u.row0 * a.ldz + at]));
+        static_cast<T *>(a.out)[u.row0 * a.HV * DV + at] = from_f32<T>(o);
+    }
+}
+
+template <typename T, int DK, int DV>
+cudaError_t launch_step(const SsmArgs &a, cudaStream_t stream) {
+    return for_sequences(a.cu, a.N, a.T, INT_MAX, [&](const SeqTable &t, long long units) {
+        trace_begin(kKernSsm, stream);
+        gdr_ssm_step_kernel<T, DK, DV><<<(unsigned)(units * a.HV), 32 * kStepWarps, 0, stream>>>(a, t);
+        trace_end(kKernSsm, stream);
+        return cudaGetLastError();
+    });
+}
+template <typename T, int DK>
+cudaError_t step_by_dv(const SsmArgs &a, cudaStream_t s) {
+    return a.dv == 32 ? launch_step<T, DK, 32>(a, s)
+                      : a.dv == 64 ? launch_step<T, DK, 64>(a, s) : launch_step<T, DK, 128>(a, s);
+}
+template <typename T>
+cudaError_t step_by_dk(const SsmArgs &a, cudaStream_t s) {
+    return a.dk == 32 ? step_by_dv<T, 32>(a, s)
+                      : a.dk == 64 ? step_by_dv<T, 64>(a, s) : step_by_dv<T, 128>(a, s);
+}
+
 template <typename T, int DK, int PASS>
 cudaError_t launch_walk(const SsmArgs &a, cudaStream_t stream) {
     return for_sequences(a.cu, a.N, a.T, a.seg_rows, [&](const SeqTable &t, long long units) {
@@ -275,9 +369,8 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
     SsmArgs a = {x, b, c, z, dt, A, D, dt_bias, h0, out, ht, nullptr, nullptr, ldx, ldb, ldc, ldz,
                  N, T, HK, HV, dk, dv, cu_seqlens, plan.seg_rows,
                  (flags & GDR_FLAG_DT_SOFTPLUS) ? 1 : 0, dtype == GDR_BF16 ? 1 : 0};
-    const auto walk = plan.longest > 1 && !(flags & GDR_FLAG_FORCE_GENERIC) && ssm_chunks_supported(a)
-                          ? launch_ssm_chunks
-                          : launch_ssm_walk;
+    const auto walk = !(flags & GDR_FLAG_FORCE_GENERIC) && ssm_chunks_supported(a) ? launch_ssm_chunks
+                                                                                   : launch_ssm_walk;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
     if (plan.bytes) {
@@ -291,6 +384,8 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
         }
         if (err == cudaSuccess) err = walk(a, 1, s);
         if (err == cudaSuccess) err = walk(a, 2, s);
+    } else if (plan.longest <= 1 && !(flags & GDR_FLAG_FORCE_GENERIC)) {
+        err = dtype == GDR_BF16 ? step_by_dk<__nv_bfloat16>(a, s) : step_by_dk<float>(a, s);
     } else {
         err = walk(a, 0, s);
     }

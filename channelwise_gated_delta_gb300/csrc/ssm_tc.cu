@@ -154,25 +154,6 @@ __device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity, uint32
     return ok != 0;
 }
 
-// two float32 operations at once
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 // (a, b) as hi + lo, two bf16 numbers each
 __device__ __forceinline__ void pair2(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack2(a, b);
@@ -266,12 +247,6 @@ __device__ __forceinline__ bool elect_one() {
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(p));
     return p != 0;
-}
-// silu
-__device__ __forceinline__ float gate(float z) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(-kLog2e * z)));
-    return z * r;
 }
 template <int DK, int PASS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -575,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 8; ++i) {
                             float2 q = mul2(ec[i >> 1], make_float2(y[2 * i], y[2 * i + 1]));
                             if (with_z) {
-                                q.x *= gate(__uint_as_float(zt[i] << 16));
-                                q.y *= gate(__uint_as_float(zt[i] & 0xffff0000u));
+                                q.x *= silu(__uint_as_float(zt[i] << 16));
+                                q.y *= silu(__uint_as_float(zt[i] & 0xffff0000u));
                             }
                             o[i] = pack2(q.x, q.y);
                         }
