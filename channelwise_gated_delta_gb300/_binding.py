@@ -581,56 +581,51 @@ def gdr_state_load(cache, scale, slots, out=None, stream=None):
     return out
 
 
-def _rows_of(name, t, lead, inner, dtype, index):
-    """The distance in elements of the rows of ``t`` [*lead, *inner], a ``dtype`` tensor on CUDA
-    device ``index`` whose rows may lie further apart than they are wide."""
+def _rows_of(name, t, shape, lead, wide, dtype, index):
+    """The distance in elements of the rows of ``t``, ``wide`` elements each, whose indices are the
+    first ``lead`` of ``shape``: a ``dtype`` tensor on CUDA device ``index`` whose rows may lie
+    further apart than they are wide."""
     if t.get_device() != index or index < 0:
         raise ValueError("%s must be a CUDA tensor%s"
                          % (name, " on cuda:%d" % index if index >= 0 else ""))
-    if t.shape != lead + inner or t.dtype is not dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError("%s must be %s %s, got %s %s"
-                         % (name, dtype, list(lead + inner), t.dtype, list(t.shape)))
-    wide = 1
-    for n in inner:
-        wide *= n
+                         % (name, dtype, list(shape), t.dtype, list(t.shape)))
     if t.is_contiguous():
         return wide
     strides, want = t.stride(), 1
-    n = len(lead)
-    for size, stride in zip(reversed(inner), reversed(strides[n:])):
-        if size != 1 and stride != want:
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and strides[i] != want:
             raise ValueError("%s must have rows of adjacent elements" % name)
-        want *= size
+        want *= shape[i]
     ld = wide
-    if lead[-1] != 1:
-        ld = strides[n - 1]
-        if n == 2 and lead[0] > 1 and strides[0] != lead[1] * ld:
+    if shape[lead - 1] != 1:
+        ld = strides[lead - 1]
+        if lead == 2 and shape[0] > 1 and strides[0] != shape[1] * ld:
             raise ValueError("%s must have its rows at one distance" % name)
-    elif n == 2 and lead[0] > 1:
+    elif lead == 2 and shape[0] > 1:
         ld = strides[0]
     if ld < wide and t.numel():
         raise ValueError("%s must have rows that do not overlap" % name)
     return max(ld, wide)
 
 
-def _sequences(lead, cu_seqlens):
-    """(offsets or None, N, T) of rows with the leading dimensions ``lead``."""
+def _sequences(shape, lead, cu_seqlens):
+    """(offsets or None, N, T) of rows whose indices are the first ``lead`` of ``shape``."""
     if cu_seqlens is None:
-        if len(lead) != 2:
+        if lead != 2:
             raise ValueError("without cu_seqlens the tensors are [B, T, ...]")
-        return None, lead[0], lead[1]
-    if len(lead) != 1:
+        return None, shape[0], shape[1]
+    if lead != 1:
         raise ValueError("with cu_seqlens the tensors are [rows, ...]")
     cu, n = _cu_array(cu_seqlens)
-    if cu[n] != lead[0]:
-        raise ValueError("cu_seqlens[-1] (%d) != number of rows (%d)" % (cu[n], lead[0]))
+    if cu[n] != shape[0]:
+        raise ValueError("cu_seqlens[-1] (%d) != number of rows (%d)" % (cu[n], shape[0]))
     return cu, n, 0
 
 
 def _optional(name, t, shape, index):
-    """The address of a float32 tensor of this shape, None for None."""
-    if t is None:
-        return None
+    """The address of a float32 tensor of this shape."""
     _given(name, t, shape, torch.float32, index)
     return t.data_ptr()
 
@@ -646,33 +641,36 @@ def gdr_short_conv(x, weight, bias=None, cu_seqlens=None, s0=None, out=None, st=
     the new state.  ``silu``: out = y / (1 + exp(-y)).  Returns (out, st), allocated when not given.
     """
     lib = load_library()
-    if x.dim() not in (2, 3) or weight.dim() != 2:
+    shape = x.shape
+    lead = len(shape) - 1
+    if not 1 <= lead <= 2 or weight.dim() != 2:
         raise ValueError("x must be [B, T, D] or [rows, D] and weight [D, W]")
-    lead, D, index = tuple(x.shape[:-1]), x.shape[-1], x.get_device()
-    code = _dtype_code(x.dtype, "x")
-    ldx = _rows_of("x", x, lead, (D,), x.dtype, index)
-    cu, n, T = _sequences(lead, cu_seqlens)
+    dtype, D, index = x.dtype, shape[lead], x.get_device()
+    code = _dtype_code(dtype, "x")
+    ldx = _rows_of("x", x, shape, lead, D, dtype, index)
+    cu, n, T = _sequences(shape, lead, cu_seqlens)
     W = weight.shape[1]
     _given("weight", weight, (D, W), torch.float32, index)
-    state = (n, W - 1, D)
+    s0_ptr = st_ptr = None
     if s0 is not None:
-        _given("s0", s0, state, x.dtype, index)
-    with _memory_of(stream):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            ldo = D
-        else:
-            ldo = _rows_of("out", out, lead, (D,), x.dtype, index)
-        if st is None:
-            if store_st:
-                st = torch.empty((n, max(W - 1, 0), D), dtype=x.dtype, device=x.device)
-        elif st is not s0:
-            _given("st", st, state, x.dtype, index)
+        _given("s0", s0, (n, W - 1, D), dtype, index)
+        s0_ptr = s0.data_ptr()
+    ldo = D if out is None else _rows_of("out", out, shape, lead, D, dtype, index)
+    if st is not None and st is not s0:
+        _given("st", st, (n, W - 1, D), dtype, index)
+    if out is None or (st is None and store_st):
+        with _memory_of(stream):
+            if out is None:
+                out = torch.empty(shape, dtype=dtype, device=x.device)
+            if st is None and store_st:
+                st = (torch.empty_like(s0) if s0 is not None else
+                      torch.empty((n, max(W - 1, 0), D), dtype=dtype, device=x.device))
+    if st is not None:
+        st_ptr = st.data_ptr()
     status = _on(index, lib.gdr_short_conv)(
-        x.data_ptr(), weight.data_ptr(), _optional("bias", bias, (D,), index),
-        None if s0 is None else s0.data_ptr(), out.data_ptr(),
-        None if st is None else st.data_ptr(), cu, n, T, D, W, ldx, ldo,
-        _stream_of(stream, index), code, GDR_FLAG_SILU if silu else 0)
+        x.data_ptr(), weight.data_ptr(), None if bias is None else _optional("bias", bias, (D,), index),
+        s0_ptr, out.data_ptr(), st_ptr, cu, n, T, D, W, ldx, ldo, _stream_of(stream, index), code,
+        GDR_FLAG_SILU if silu else 0)
     if status != GDR_OK:
         _check(lib, status)
     return out, st
@@ -702,44 +700,50 @@ def gdr_qk_norm(q, k, weight_q=None, weight_k=None, positions=None, freqs=None, 
     rotated, as pairs (i, i + half), or neighbours if ``interleaved``.  ``out_q=q`` and
     ``out_k=k`` work in place.  Returns (out_q, out_k), allocated when not given."""
     lib = load_library()
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    shape, kshape = q.shape, k.shape
+    lead = len(shape) - 2
+    if not 1 <= lead <= 2 or len(kshape) != lead + 2:
         raise ValueError("q and k must be [B, T, H, d] or [rows, H, d]")
-    if norm not in ("l2", "rms"):
+    if norm != "l2" and norm != "rms":
         raise ValueError('norm must be "l2" or "rms"')
-    lead, index = tuple(q.shape[:-2]), q.get_device()
-    HQ, d = q.shape[-2:]
-    HK = k.shape[-2]
-    code = _dtype_code(q.dtype, "q and k")
-    ldq = _rows_of("q", q, lead, (HQ, d), q.dtype, index)
-    ldk = _rows_of("k", k, lead, (HK, d), q.dtype, index)
-    if (positions is None) != (freqs is None):
-        raise ValueError("a rotation needs positions and freqs")
-    d_rot = 0
-    if freqs is not None:
+    dtype, index = q.dtype, q.get_device()
+    HQ, d, HK = shape[lead], shape[lead + 1], kshape[lead]
+    code = _dtype_code(dtype, "q and k")
+    rows = shape[0] if lead == 1 else shape[0] * shape[1]
+    if kshape[:lead] != shape[:lead] or kshape[lead + 1] != d:
+        raise ValueError("k must match q in rows and d")
+    ldq = _rows_of("q", q, shape, lead, HQ * d, dtype, index)
+    ldk = _rows_of("k", k, kshape, lead, HK * d, dtype, index)
+    d_rot, pos_ptr, freq_ptr = 0, None, None
+    if freqs is not None or positions is not None:
+        if freqs is None or positions is None:
+            raise ValueError("a rotation needs positions and freqs")
         if freqs.dim() != 1:
             raise ValueError("freqs must be [d_rot / 2]")
         d_rot = 2 * freqs.shape[0]
         _given("freqs", freqs, (d_rot // 2,), torch.int64, index)
-        _given("positions", positions, lead, torch.int32, index)
-    with _memory_of(stream):
-        if out_q is None:
-            out_q, ldoq = torch.empty(q.shape, dtype=q.dtype, device=q.device), HQ * d
-        else:
-            ldoq = _rows_of("out_q", out_q, lead, (HQ, d), q.dtype, index)
-        if out_k is None:
-            out_k, ldok = torch.empty(k.shape, dtype=q.dtype, device=q.device), HK * d
-        else:
-            ldok = _rows_of("out_k", out_k, lead, (HK, d), q.dtype, index)
-    rows = 1
-    for n in lead:
-        rows *= n
+        _given("positions", positions, shape[:lead], torch.int32, index)
+        if d_rot:
+            pos_ptr, freq_ptr = positions.data_ptr(), freqs.data_ptr()
+    ldoq, ldok = HQ * d, HK * d
+    if out_q is not None:
+        ldoq = ldq if out_q is q else _rows_of("out_q", out_q, shape, lead, HQ * d, dtype, index)
+    if out_k is not None:
+        ldok = ldk if out_k is k else _rows_of("out_k", out_k, kshape, lead, HK * d, dtype, index)
+    if out_q is None or out_k is None:
+        with _memory_of(stream):
+            if out_q is None:
+                out_q = torch.empty(shape, dtype=dtype, device=q.device)
+            if out_k is None:
+                out_k = torch.empty(kshape, dtype=dtype, device=q.device)
     flags = (GDR_FLAG_RMS_NORM if norm == "rms" else 0) | (
         GDR_FLAG_ROPE_INTERLEAVED if interleaved else 0)
     status = _on(index, lib.gdr_qk_norm)(
-        q.data_ptr(), k.data_ptr(), _optional("weight_q", weight_q, (d,), index),
-        _optional("weight_k", weight_k, (d,), index), positions.data_ptr() if d_rot else None,
-        freqs.data_ptr() if d_rot else None, out_q.data_ptr(), out_k.data_ptr(), rows, HQ, HK, d,
-        d_rot, ldq, ldk, ldoq, ldok, eps, q_scale, _stream_of(stream, index), code, flags)
+        q.data_ptr(), k.data_ptr(),
+        None if weight_q is None else _optional("weight_q", weight_q, (d,), index),
+        None if weight_k is None else _optional("weight_k", weight_k, (d,), index), pos_ptr, freq_ptr,
+        out_q.data_ptr(), out_k.data_ptr(), rows, HQ, HK, d, d_rot, ldq, ldk, ldoq, ldok, eps,
+        q_scale, _stream_of(stream, index), code, flags)
     if status != GDR_OK:
         _check(lib, status)
     return out_q, out_k
@@ -763,47 +767,57 @@ def gdr_ssm_forward(x, b, c, dt, a, d=None, z=None, dt_bias=None, cu_seqlens=Non
     place of [B, T].  h0, ht [B, HV, dk, dv] f32 as in gdr_forward (``ht=h0`` updates in place;
     ``store_ht=False`` skips it).  d, z, dt_bias, h0 may be None.  Returns (out, ht)."""
     lib = load_library()
-    if x.dim() not in (3, 4) or b.dim() != x.dim():
+    shape, bshape = x.shape, b.shape
+    lead = len(shape) - 2
+    if not 1 <= lead <= 2 or len(bshape) != lead + 2:
         raise ValueError("x and b must be [B, T, H, d] or [rows, H, d]")
-    lead, index = tuple(x.shape[:-2]), x.get_device()
-    HV, dv = x.shape[-2:]
-    HK, dk = b.shape[-2:]
-    code = _dtype_code(x.dtype, "x, b and c")
-    ldx = _rows_of("x", x, lead, (HV, dv), x.dtype, index)
-    ldb = _rows_of("b", b, lead, (HK, dk), x.dtype, index)
-    ldc = _rows_of("c", c, lead, (HK, dk), x.dtype, index)
-    ldz = 0 if z is None else _rows_of("z", z, lead, (HV, dv), x.dtype, index)
-    _given("dt", dt, lead + (HV,), torch.float32, index)
+    dtype, index = x.dtype, x.get_device()
+    HV, dv, HK, dk = shape[lead], shape[lead + 1], bshape[lead], bshape[lead + 1]
+    code = _dtype_code(dtype, "x, b and c")
+    if bshape[:lead] != shape[:lead]:
+        raise ValueError("b must match x in rows")
+    ldx = _rows_of("x", x, shape, lead, HV * dv, dtype, index)
+    ldb = _rows_of("b", b, bshape, lead, HK * dk, dtype, index)
+    ldc = _rows_of("c", c, bshape, lead, HK * dk, dtype, index)
+    ldz, z_ptr = 0, None
+    if z is not None:
+        ldz, z_ptr = _rows_of("z", z, shape, lead, HV * dv, dtype, index), z.data_ptr()
+    _given("dt", dt, shape[:lead + 1], torch.float32, index)
     _given("a", a, (HV,), torch.float32, index)
-    cu, n, T = _sequences(lead, cu_seqlens)
-    state = (n, HV, dk, dv)
-    h0_ptr = _optional("h0", h0, state, index)
+    cu, n, T = _sequences(shape, lead, cu_seqlens)
+    h0_ptr = ht_ptr = None
+    if h0 is not None:
+        h0_ptr = _optional("h0", h0, (n, HV, dk, dv), index)
+    if ht is not None and ht is not h0:
+        _given("ht", ht, (n, HV, dk, dv), torch.float32, index)
+    if out is not None:
+        _given("out", out, shape, dtype, index)
     if softplus:
         flags |= GDR_FLAG_DT_SOFTPLUS
-    need = int(_on(index, lib.gdr_ssm_workspace_bytes)(cu, n, T, HK, HV, dk, dv, code, flags))
-    with _memory_of(stream):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _given("out", out, x.shape, x.dtype, index)
-        if ht is None:
-            if store_ht:
-                ht = torch.empty(state, dtype=torch.float32, device=x.device)
-        elif ht is not h0:
-            _given("ht", ht, state, torch.float32, index)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    ws, ws_bytes = None, 0
+    need, ws_ptr, ws_bytes = 0, None, 0
+    if T != 1:   # single tokens need no workspace
+        need = _on(index, lib.gdr_ssm_workspace_bytes)(cu, n, T, HK, HV, dk, dv, code, flags)
+    if out is None or (ht is None and store_ht) or need:
+        with _memory_of(stream):
+            if out is None:
+                out = torch.empty(shape, dtype=dtype, device=x.device)
+            if ht is None and store_ht:
+                ht = (torch.empty_like(h0) if h0 is not None else
+                      torch.empty((n, HV, dk, dv), dtype=torch.float32, device=x.device))
+            if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     if need:
         if workspace.get_device() != index:
             raise ValueError("workspace must be a CUDA tensor on cuda:%d" % index)
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if ht is not None:
+        ht_ptr = ht.data_ptr()
     status = _on(index, lib.gdr_ssm_forward)(
         x.data_ptr(), b.data_ptr(), c.data_ptr(), dt.data_ptr(), a.data_ptr(),
-        _optional("d", d, (HV,), index), None if z is None else z.data_ptr(),
-        _optional("dt_bias", dt_bias, (HV,), index), h0_ptr, out.data_ptr(),
-        None if ht is None else ht.data_ptr(), cu, n, T, HK, HV, dk, dv, ldx, ldb, ldc, ldz,
-        _stream_of(stream, index), code, ws, ws_bytes, flags)
+        None if d is None else _optional("d", d, (HV,), index), z_ptr,
+        None if dt_bias is None else _optional("dt_bias", dt_bias, (HV,), index), h0_ptr,
+        out.data_ptr(), ht_ptr, cu, n, T, HK, HV, dk, dv, ldx, ldb, ldc, ldz,
+        _stream_of(stream, index), code, ws_ptr, ws_bytes, flags)
     if status != GDR_OK:
         _check(lib, status)
     return out, ht

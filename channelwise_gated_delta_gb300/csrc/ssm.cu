@@ -277,14 +277,59 @@ struct Plan {
     size_t off_log, off_h0;
 };
 
-Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, unsigned flags) {
+// SMs of the current device; 0 without one.
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return sms;
+}
+
+// Rows of a segment: few heads leave SMs idle while a long sequence is walked,
+// so walks are cut where that is estimated to be faster.  Costs are in rows of
+// a full walk; a walk to the end state alone, the second launch and the start
+// from the segments before were measured (chunks: one CTA an SM; walk: kWalkCtas
+// of them, a token's latency being the same up to there).
+int choose_segment(const int *cu, int N, int T, int HV, int dv, int longest, bool chunks) {
+    constexpr int kWalkCtas = 4;
+    const int sms = sm_count(), grain = chunks ? 64 : 16;
+    const long long per = (long long)HV * (chunks ? 1 : dv / 32);
+    const long long slots = (long long)sms * (chunks ? 1 : kWalkCtas);
+    if (sms == 0 || longest < 4 * grain || N * per >= slots) return INT_MAX;
+    const double state_only = 0.5, launch = chunks ? 256 : 32, start = chunks ? 24 : 4;
+    double best = longest;
+    int rows = INT_MAX;
+    for (int cut = 2; cut <= 64; ++cut) {
+        const int r = ((longest + cut - 1) / cut + grain - 1) / grain * grain;
+        if (r >= longest) continue;
+        const long long units = count_units(cu, N, T, r), after = units - N;
+        const double cost = (double)((units * per + slots - 1) / slots) * r +
+                            state_only * (double)((after * per + slots - 1) / slots) * r + launch +
+                            start * (longest / r);
+        if (cost < 0.9 * best) {
+            best = cost;
+            rows = r;
+        }
+    }
+    return rows;
+}
+
+Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, int dtype, unsigned flags) {
     Plan p = {cu ? 0 : T, INT_MAX, N, 0, 0, 0};
     const int forced = (int)((flags >> 8) & 0xffu);
     int &longest = p.longest;
     for (int n = 0; cu && n < N; ++n) longest = longest > cu[n + 1] - cu[n] ? longest : cu[n + 1] - cu[n];
-    if (forced >= 2 && !(flags & GDR_FLAG_NO_SEGMENTS) && longest > 64) {
-        const int rows = ((longest + forced - 1) / forced + 63) / 64 * 64;
-        if (rows < longest) p.seg_rows = rows;
+    if (!(flags & GDR_FLAG_NO_SEGMENTS) && longest > 64) {
+        if (forced >= 2) {
+            const int rows = ((longest + forced - 1) / forced + 63) / 64 * 64;
+            if (rows < longest) p.seg_rows = rows;
+        } else if (forced == 0) {
+            p.seg_rows = choose_segment(cu, N, T, HV, dv, longest,
+                                        dtype == GDR_BF16 && !(flags & GDR_FLAG_FORCE_GENERIC));
+        }
     }
     if (p.seg_rows != INT_MAX) {
         p.units = count_units(cu, N, T, p.seg_rows);
@@ -323,7 +368,7 @@ extern "C" GDR_API size_t gdr_ssm_workspace_bytes(const int *cu_seqlens, int N, 
                                                   unsigned flags) {
     using namespace gdr;
     if (check_shape(cu_seqlens, N, T, HK, HV, dk, dv, dtype, flags) != GDR_OK || N == 0) return 0;
-    return make_plan(cu_seqlens, N, T, HV, dk, dv, flags).bytes;
+    return make_plan(cu_seqlens, N, T, HV, dk, dv, dtype, flags).bytes;
 }
 
 extern "C" GDR_API gdr_status gdr_ssm_forward(
@@ -359,7 +404,7 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
         if (rows_overlap(o, r) || rows_overlap(e, r)) return GDR_ERR_ALIAS;
     if (rows_overlap(o, h) || rows_overlap(o, e) || (h0 != ht && rows_overlap(e, h)))
         return GDR_ERR_ALIAS;
-    const Plan plan = make_plan(cu_seqlens, N, T, HV, dk, dv, flags);
+    const Plan plan = make_plan(cu_seqlens, N, T, HV, dk, dv, dtype, flags);
     if (plan.bytes) {
         if (!workspace || workspace_bytes < plan.bytes) return GDR_ERR_WORKSPACE;
         if ((uintptr_t)workspace & 255u) return GDR_ERR_ALIGN;

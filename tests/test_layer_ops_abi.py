@@ -1,6 +1,7 @@
 """What gdr_short_conv, gdr_qk_norm and gdr_ssm_forward refuse: on the host, before anything is
 enqueued (CPU only: fake pointers, no compute call); and what the Python entries check."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -168,7 +169,7 @@ def test_distances_of_rows():
     rows = _binding._rows_of
     wide = torch.zeros(3, 5, 100)
     bf = torch.float32
-    at = lambda t, *inner: rows("t", OnGpu(t), tuple(t.shape[:t.dim() - len(inner)]), inner, bf, 0)
+    at = lambda t, *inner: rows("t", OnGpu(t), t.shape, t.dim() - len(inner), math.prod(inner), bf, 0)
     assert at(wide, 100) == 100 and at(wide[..., :64], 64) == 100
     assert at(wide[..., 4:68].unflatten(-1, (2, 32)), 2, 32) == 100
     assert at(wide[:, :1, :64], 64) == 500 and at(wide[:1, :, :64], 64) == 100
