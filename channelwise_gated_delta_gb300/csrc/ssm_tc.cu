@@ -64,9 +64,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kWx0 = 16, kOut0 = 20, kScore0 = 24, kProducer = 26, kIssueState = 27, kIssueY = 30;
 constexpr int kStages = 3;
 constexpr int kRing = 8;  // chunks whose scalars are held
-// a wait's limit: tries of up to kTryNs each, two seconds in all
-constexpr uint32_t kTryNs = 2000;
-constexpr uint32_t kTries = 1u << 20;
+// a wait's limit: tries, of some 50 cycles each at least
+constexpr int kTries = 1 << 25;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -129,29 +128,25 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&h);
 }
-// Waits for a phase of the barrier in at most kTries tries of up to kTryNs,
-// or until the CTA's abort flag is set.  One small loop: the kernel's twenty
-// warps run seven different programs out of one instruction cache, and it ran
-// at 0.65 of its speed while their code took 88 KB instead of 60.
-__device__ __forceinline__ bool wait_tries(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
-    uint32_t ok;
+// Waits for a phase of the barrier; where it has not come in kTries tries (a
+// second or more), sets the CTA's abort flag and goes on: every warp looks at
+// the flag once a chunk.  As few instructions as that takes: the kernel's warps
+// run seven different programs out of one instruction cache, and it ran at 0.65
+// of its speed while their code took 88 KB instead of 60.
+__device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b32 n, q;\n\t"
-        "mov.b32 n, 0;\n"
+        "{\n\t.reg .pred p;\n\t.reg .b32 n;\n\t"
+        "mov.b32 n, %3;\n"
         "TRY_%=:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
         "@p bra DONE_%=;\n\t"
-        "ld.volatile.shared.b32 q, [%5];\n\t"
-        "add.u32 n, n, 1;\n\t"
-        "setp.eq.u32 p, q, 0;\n\t"
-        "setp.lt.and.u32 p, n, %4, p;\n\t"
-        "@p bra TRY_%=;\n"
-        "DONE_%=:\n\t}"
-        : "=&r"(ok)
-        : "r"(bar), "r"(parity), "r"(kTryNs), "r"(kTries), "r"(abort_flag)
+        "add.s32 n, n, -1;\n\t"
+        "setp.ne.s32 p, n, 0;\n\t"
+        "@p bra TRY_%=;\n\t"
+        "st.volatile.shared.b32 [%2], 1;\n"
+        "DONE_%=:\n\t}" ::"r"(bar),
+        "r"(parity), "r"(abort_flag), "n"(kTries)
         : "memory");
-    return ok != 0;
 }
 
 // (a, b) as hi + lo, two bf16 numbers each
@@ -193,19 +188,24 @@ __device__ __forceinline__ void stsm4_t(uint32_t at, const uint32_t (&r)[4]) {
 // float32 (registers 4 j + {0, 1}: lane / 4 of the 16, columns 8 j + 2 (lane %
 // 4) + {0, 1}; + 2: eight lanes on), and 16 columns of pairs (register 2 j:
 // lane / 4, column 4 j + lane % 4; + 1: eight lanes on).
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t at, float (&v)[16]) {
-    uint32_t r[16];
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15])
         : "r"(at)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// what such a load has brought, once it is there
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_16x128(uint32_t at, const uint32_t (&r)[8]) {
     asm volatile(
@@ -298,15 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *slot;
-    // A wait that runs out sets the CTA's abort flag; from then on every wait
-    // that is not already over returns, and the loops run out.
     const uint32_t bar0 = smem_u32(bars), abort0 = smem_u32(smem + kAbort);
-    auto wait = [&](int id, uint32_t parity) {
-        if (!wait_tries(bar0 + 8 * id, parity & 1, abort0)) {
-            if (!*abort_flag && err) atomicExch(err, 1);
-            *abort_flag = 1;
-        }
-    };
+    auto wait = [&](int id, uint32_t parity) { wait_bounded(bar0 + 8 * id, parity & 1, abort0); };
     auto scal = [&](int c, uint32_t what) {
         return reinterpret_cast<float *>(smem + kScal + (c & (kRing - 1)) * kScalBytes + what);
     };
@@ -355,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < NH; ++i, e += dv) S[i] = fmaf(keep, S[i], *e);
             }
-        for (int c = 0; c < NC; ++c, at.next()) {
+        for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
             if (OUT) {
                 if (c > 0) wait(SFREE, c - 1);
                 if (on) {
@@ -422,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = lane & 7;
         const uint32_t x0 = smem_u32(smem) + kX + (p0 >> 6) * 8192 + ((lane >> 4) * 8 + row) * 128;
         const int unit = ((p0 & 63) >> 3) + ((lane >> 3) & 1);
-        for (int c = 0; c < NC; ++c, at.next()) {
+        for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
             const int st = at.st, L = rows_in(c);
             wait(FULL + st, at.ph);
             if (L < kC) wait(FIX, 0);
@@ -498,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (gated && NC > 0) fetch(0);
             uint32_t beyond = 0;  // chunks beyond r's range so far
-            for (int c = 0; c < NC; ++c) {
+            for (int c = 0; c < NC && !*abort_flag; ++c) {
                 const int L = rows_in(c);
                 const uint32_t ty = tl + kTmY + 64 * (c & 1);
                 if (gated) {
@@ -533,26 +526,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         const int hh = k & 1, t32 = k >> 1;  // half of the columns, of the tokens
-                        const uint32_t at = blk + (c & 1) * 16384 + t32 * 2048 + (((lane >> 3 & 1) + 2 * hh) ^ xr) * 16;
-                        float2 ec[4];
+                        const uint32_t at =
+                            blk + (c & 1) * 16384 + t32 * 2048 + (((lane >> 3 & 1) + 2 * hh) ^ xr) * 16;
+                        uint32_t y[16];
+                        tmem_ld_16x256(ty + ((uint32_t)(16 * hh) << 16) + 32 * t32, y);
+                        // meanwhile the factors: exp(cum - r), times silu(z)
+                        float2 f[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            ec[j] = *reinterpret_cast<const float2 *>(e + 32 * t32 + 8 * j + 2 * (lane & 3));
-                        uint32_t zt[8];
+                            f[2 * j] = f[2 * j + 1] = *reinterpret_cast<const float2 *>(
+                                e + 32 * t32 + 8 * j + 2 * (lane & 3));
                         if (with_z) {
+                            uint32_t zt[8];
                             ldsm4_t(at, *reinterpret_cast<uint32_t (*)[4]>(zt));
                             ldsm4_t(at + 1024, *reinterpret_cast<uint32_t (*)[4]>(zt + 4));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                f[i].x *= silu(__uint_as_float(zt[i] << 16));
+                                f[i].y *= silu(__uint_as_float(zt[i] & 0xffff0000u));
+                            }
                         }
-                        float y[16];
-                        tmem_ld_16x256(ty + ((uint32_t)(16 * hh) << 16) + 32 * t32, y);
+                        tmem_ld_wait(y);
                         uint32_t o[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            float2 q = mul2(ec[i >> 1], make_float2(y[2 * i], y[2 * i + 1]));
-                            if (with_z) {
-                                q.x *= silu(__uint_as_float(zt[i] << 16));
-                                q.y *= silu(__uint_as_float(zt[i] & 0xffff0000u));
-                            }
+                            const float2 q = mul2(f[i], make_float2(__uint_as_float(y[2 * i]),
+                                                                    __uint_as_float(y[2 * i + 1])));
                             o[i] = pack2(q.x, q.y);
                         }
                         stsm4_t(at, *reinterpret_cast<const uint32_t (*)[4]>(o));
@@ -588,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int g0 = ((warp - kScore0) >> 2) << sw;
             const uint32_t tl = tmem + ((uint32_t)(32 * sw) << 16);
             const float D = a.D ? a.D[hv] : 0.f;
-            for (int c = 0; c < NC; ++c, at.next()) {
+            for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
                 const int L = rows_in(c);
                 wait(FULL + at.st, at.ph);
                 wait(GRAM, c);
@@ -649,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float d0 = dt_at(2 * lane), d1 = dt_at(2 * lane + 1);
         double total = 0.0;  // log2 of the unit's decay
         int armed = -1;
-        for (int c = 0; c < NC; ++c, at.next()) {
+        for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
             const int st = at.st, t0 = c * kC, t = t0 + 2 * lane;
             float s0 = ssm_step(d0, bias, a.softplus), s1 = ssm_step(d1, bias, a.softplus);
             s0 = t < T ? s0 : 0.f;
@@ -674,8 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float c1 = c0 + l1, f0 = f1 + l1;
             const float all0 = __shfl_sync(0xffffffffu, c1, 15), all1 = __shfl_sync(0xffffffffu, c1, 31);
             if (PASS == 1) total += (double)all0 + all1;
-            if (c >= kStages) wait(EMPTY + st, at.ph ^ 1);
-            if (*abort_flag) break;
             float *q = scal(c, 0) + 2 * lane;
             auto put = [&](uint32_t what, float x, float y) {
                 *reinterpret_cast<float2 *>(q + what / 4) = make_float2(x, y);
@@ -709,6 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 end[1] = fast_exp2(r);
                 end[2] = far ? 1.f : 0.f;
             }
+            // the scalars go ahead of the stage: theirs are as many chunks more as
+            // the outputs may lag behind
+            if (c >= kStages) wait(EMPTY + st, at.ph ^ 1);
+            if (*abort_flag) break;
             __syncwarp();
             if (lane == 0) {
                 uint64_t *bar = &bars[FULL + st];
@@ -771,13 +772,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(FULL, 0);
             gram(0);
         }
-        for (int c = 0; c < NC; ++c) {
+        for (int c = 0; c < NC && !*abort_flag; ++c) {
             const int st = at.st;
             const uint64_t o = (uint64_t)(st * (kStage >> 4));
             at.next();
             wait(WX + (c & 1), c >> 1);
             wait(DFREE, c);
-            if (*abort_flag) break;
             tc_fence_after_sync();
             if (elect_one()) {
                 // hi, then lo, against the same rows
@@ -806,13 +806,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dC = smem_desc_sw128(sb + kCm, 16, 1024), dXt = smem_desc_sw128(sb + kX, 8192, 1024);
         const uint64_t dM = smem_desc(sb + kM, 128, kC * 16);
         uint32_t beyond = 0;
-        for (int c = 0; c < NC; ++c, at.next()) {
+        for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
             const uint64_t o = (uint64_t)(at.st * (kStage >> 4)), m = dM + (uint64_t)((c & 1) * 1024);
             const uint32_t y = tmem + kTmY + 64 * (c & 1);
             wait(FULL + at.st, at.ph);
             wait(SFULL, c);
             if (c >= 2) wait(YFREE + (c & 1), (c >> 1) - 1);
-            if (*abort_flag) break;
             const bool far = scal(c, kEnd)[2] != 0.f;
             tc_fence_after_sync();
             if (elect_one()) {
@@ -840,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (tid == 0 && *abort_flag && err) atomicExch(err, 1);
     if (warp == 0) tmem_dealloc(tmem, kTmCols);
 }
 
