@@ -36,8 +36,8 @@
 //     20-23  outputs: Y exp(cum - r), times silu(z)
 //     24, 25, 28, 29  scores: rows of G to rows of M (G's 64 rows are TMEM lanes
 //            0-63, which only warps 4 n and 4 n + 1 can read)
-//     26     producer: TMA of x, b, c three chunks ahead, and the chunk's
-//            scalars (steps, prefix sums, decays) two tokens a lane
+//     26     the chunk's scalars (steps, prefix sums, decays), two tokens a lane
+//     31     TMA of x, b and c, up to three chunks ahead
 //     27, 30 issue the MMAs (one thread each): G and dS; Y.  An MMA takes its
 //            thread as long as the tensor cores (32 to 64 cycles each), and a
 //            thread that waits for one product's inputs feeds no other
@@ -59,9 +59,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 64;
-constexpr int kWarps = 31;
+constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWx0 = 16, kOut0 = 20, kScore0 = 24, kProducer = 26, kIssueState = 27, kIssueY = 30;
+constexpr int kWx0 = 16, kOut0 = 20, kScore0 = 24, kScalars = 26, kIssueState = 27, kIssueY = 30,
+              kLoads = 31;
 constexpr int kStages = 3;
 constexpr int kRing = 8;  // chunks whose scalars are held
 // a wait's limit: tries, of some 50 cycles each at least
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   i == YFREE || i == YFREE + 1 || i == YSCALED
                               ? 128
                           : i == DFREE || i == SFULL               ? 4 * DK
-                          : i >= EMPTY && i < EMPTY + kStages && OUT ? 2
+                          : i < EMPTY || (i < EMPTY + kStages && OUT) ? 2
                                                                      : 1;
             mbar_init(&bars[i], n);
         }
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp != kProducer && warp != kIssueState && warp != kIssueY) {
+    } else if (warp != kScalars && warp != kIssueState && warp != kIssueY && warp != kLoads) {
         // ================= scores: lane = token t of the chunk
         if (OUT) {
             const int sw = warp & 1, t = 32 * sw + lane;
@@ -638,18 +639,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[MFULL + (c & 1)]);
             }
         }
-    } else if (warp == kProducer) {
-        // ================= TMA and scalars: tokens 2 lane and 2 lane + 1
+    } else if (warp == kLoads) {
+        // ================= TMA
         const int nx = dv > 64 ? 2 : 1, nb = DK > 64 ? 2 : 1;
+        int armed = -1;
+        for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
+            const int st = at.st;
+            if (c >= kStages) wait(EMPTY + st, at.ph ^ 1);
+            if (*abort_flag) break;
+            if (lane == 0) {
+                uint64_t *bar = &bars[FULL + st];
+                unsigned char *to = smem + st * kStage;
+                mbar_arrive_expect_tx(bar, (uint32_t)(nx + (OUT ? 2 : 1) * nb) * 8192u);
+                const int row = (int)(row0 + c * kC);
+#pragma unroll 1
+                for (int k = 0; k < nx; ++k)
+                    tma_load_2d(to + kX + 8192 * k, &maps.x, hv * dv + 64 * k, row, bar);
+#pragma unroll 1
+                for (int k = 0; k < nb; ++k) {
+                    tma_load_2d(to + kB + 8192 * k, &maps.b, hk * DK + 64 * k, row, bar);
+                    if (OUT) tma_load_2d(to + kCm + 8192 * k, &maps.c, hk * DK + 64 * k, row, bar);
+                }
+                armed = c;
+            }
+            __syncwarp();
+            const int L = rows_in(c);
+            if (L < kC) {
+                // the last chunk's rows behind the end hold other sequences'
+                // values: zeros, since 0 times those may not be 0
+                wait(FULL + st, at.ph);
+#pragma unroll 1
+                for (int k = lane; k < (kC - L) * 16; k += 32) {
+                    const int r = L + k / 16;
+                    const uint32_t o = ((k >> 3) & 1) * 8192 + r * 128 + (k & 7) * 16;
+                    *reinterpret_cast<uint4 *>(smem + st * kStage + kX + o) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(smem + st * kStage + kB + o) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[FIX]);
+            }
+        }
+        if (*abort_flag && lane == 0)  // copies in flight land before the CTA leaves
+#pragma unroll 1
+            for (int c = armed < kStages ? 0 : armed - kStages + 1; c <= armed; ++c)
+                mbar_wait_bounded(&bars[FULL + c % kStages], (c / kStages) & 1, kWaitNs);
+    } else if (warp == kScalars) {
+        // ================= scalars: tokens 2 lane and 2 lane + 1
         const float A2 = a.A[hv] * kLog2e, bias = a.dt_bias ? a.dt_bias[hv] : 0.f;
         const float D = a.D ? a.D[hv] : 0.f;
         const float *dt = a.dt + row0 * a.HV + hv;
         auto dt_at = [&](int t) { return t < T ? __ldg(dt + (long long)t * a.HV) : 0.f; };
         float d0 = dt_at(2 * lane), d1 = dt_at(2 * lane + 1);
         double total = 0.0;  // log2 of the unit's decay
-        int armed = -1;
         for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
-            const int st = at.st, t0 = c * kC, t = t0 + 2 * lane;
+            const int t = c * kC + 2 * lane;
             float s0 = ssm_step(d0, bias, a.softplus), s1 = ssm_step(d1, bias, a.softplus);
             s0 = t < T ? s0 : 0.f;
             s1 = t + 1 < T ? s1 : 0.f;
@@ -706,51 +750,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 end[1] = fast_exp2(r);
                 end[2] = far ? 1.f : 0.f;
             }
-            // the scalars go ahead of the stage: theirs are as many chunks more as
-            // the outputs may lag behind
-            if (c >= kStages) wait(EMPTY + st, at.ph ^ 1);
-            if (*abort_flag) break;
+            // there are as many more of these than stages as the outputs may lag
+            // behind, but a stage's barrier counts one chunk at a time
+            if (c >= kStages) wait(EMPTY + at.st, at.ph ^ 1);
             __syncwarp();
-            if (lane == 0) {
-                uint64_t *bar = &bars[FULL + st];
-                unsigned char *to = smem + st * kStage;
-                mbar_arrive_expect_tx(bar, (uint32_t)(nx + (OUT ? 2 : 1) * nb) * 8192u);
-                const int row = (int)(row0 + t0);
-#pragma unroll 1
-                for (int k = 0; k < nx; ++k)
-                    tma_load_2d(to + kX + 8192 * k, &maps.x, hv * dv + 64 * k, row, bar);
-#pragma unroll 1
-                for (int k = 0; k < nb; ++k) {
-                    tma_load_2d(to + kB + 8192 * k, &maps.b, hk * DK + 64 * k, row, bar);
-                    if (OUT) tma_load_2d(to + kCm + 8192 * k, &maps.c, hk * DK + 64 * k, row, bar);
-                }
-                armed = c;
-            }
-            __syncwarp();
-            const int L = rows_in(c);
-            if (L < kC) {
-                // the last chunk's rows behind the end hold other sequences'
-                // values: zeros, since 0 times those may not be 0
-                wait(FULL + st, at.ph);
-#pragma unroll 1
-                for (int k = lane; k < (kC - L) * 16; k += 32) {
-                    const int r = L + k / 16;
-                    const uint32_t o = ((k >> 3) & 1) * 8192 + r * 128 + (k & 7) * 16;
-                    *reinterpret_cast<uint4 *>(smem + st * kStage + kX + o) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(smem + st * kStage + kB + o) = make_uint4(0, 0, 0, 0);
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[FIX]);
-            }
+            if (lane == 0) mbar_arrive(&bars[FULL + at.st]);
         }
         if (PASS == 1 && lane == 0) {
             a.seg_log[(size_t)unit * a.HV + hv] = (float)(total * 0.6931471805599453);
         }
-        if (*abort_flag && lane == 0)  // copies in flight land before the CTA leaves
-#pragma unroll 1
-            for (int c = armed < kStages ? 0 : armed - kStages + 1; c <= armed; ++c)
-                mbar_wait_bounded(&bars[FULL + c % kStages], (c / kStages) & 1, kWaitNs);
     } else if (warp == kIssueState) {
         // ================= MMA issue: G and dS.  The warp waits as one, one lane issues
         constexpr uint32_t idG = idesc_bf16(128, kC, false, false, false);
