@@ -413,7 +413,7 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     SsmArgs a = {x, b, c, z, dt, A, D, dt_bias, h0, out, ht, nullptr, nullptr, ldx, ldb, ldc, ldz,
                  N, T, HK, HV, dk, dv, cu_seqlens, plan.seg_rows,
-                 (flags & GDR_FLAG_DT_SOFTPLUS) ? 1 : 0, dtype == GDR_BF16 ? 1 : 0};
+                 (flags & GDR_FLAG_DT_SOFTPLUS) ? 1 : 0, dtype == GDR_BF16 ? 1 : 0, 0};
     const auto walk = !(flags & GDR_FLAG_FORCE_GENERIC) && ssm_chunks_supported(a) ? launch_ssm_chunks
                                                                                    : launch_ssm_walk;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

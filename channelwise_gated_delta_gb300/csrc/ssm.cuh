@@ -20,6 +20,7 @@ struct SsmArgs {
     int seg_rows;    // rows of a unit; INT_MAX: not cut
     int softplus;
     int bf16;
+    int z_tma;  // z can be read by TMA (set by launch_ssm_chunks)
 };
 
 // step = softplus(dt + bias) (or dt + bias as it is)

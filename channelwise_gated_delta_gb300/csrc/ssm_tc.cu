@@ -81,7 +81,8 @@ constexpr uint32_t kScal = kM + 2 * 16384;          // [kRing] of the following
 constexpr uint32_t kE = 0, kW = 256, kV = 512, kDiag = 768, kCum = 1024, kStep = 1280, kEnd = 1536;
 constexpr uint32_t kScalBytes = 1552;
 constexpr float kRange = 80.f;
-constexpr uint32_t kOut = kScal + kRing * kScalBytes;  // [2][4 warps] [64 t][32] z, then outputs
+constexpr uint32_t kOut = (kScal + kRing * kScalBytes + 1023) / 1024 * 1024;  // [2][4 warps] [64 t][32]
+                                                                              // z, then outputs
 constexpr uint32_t kBars = kOut + 2 * 16384;
 enum {
     FULL = 0,               // [3] x, b, c of a chunk in, and its scalars
@@ -102,7 +103,8 @@ enum {
     YSCALED = YFREE + 2,     // in a chunk beyond r's range YDONE is the part from the state;
     YPART,                   // that is rescaled, and the rest added to it
     LAST,                    // [2] all done
-    kNumBars = LAST + 2
+    ZFULL = LAST + 2,        // [2][4 warps] z in
+    kNumBars = ZFULL + 8
 };
 constexpr uint32_t kSlot = kBars + 8 * kNumBars;
 constexpr uint32_t kAbort = kSlot + 4;
@@ -113,7 +115,7 @@ static_assert(kSmem <= 232448 && kOut % 16 == 0 && kBars % 8 == 0, "shared memor
 constexpr uint32_t kTmG = 0, kTmY = 64, kTmS = 192, kTmD = 256, kTmW = 384, kTmCols = 512;
 
 struct Maps {
-    CUtensorMap x, b, c;
+    CUtensorMap x, b, c, z, out;
 };
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int c0, int c1,
@@ -123,6 +125,13 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int c0, 
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const void *map, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(smem_u32(src))
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -214,11 +223,9 @@ __device__ __forceinline__ void tmem_st_16x128(uint32_t at, const uint32_t (&r)[
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void cp_async_wait_but_one() {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+// waits until all but the latest of the thread's bulk stores have read shared memory
+__device__ __forceinline__ void bulk_wait_read_but_one() {
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 // `steps` products of 16 along K, the operands' descriptors (of which only the
 // address, in the low half, moves) in steps of their own; one of A's is
@@ -452,55 +459,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (OUT) {
             const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
             const bool on = 32 * (warp & 3) < dv;
-            // the warp's 32 columns of a chunk pass through shared memory, so that
-            // they go out (and z comes in) 16 bytes at a time: lane = row
-            // lane / 4 of eight, 16 bytes lane % 4 of it.  There a row's four 16
-            // bytes are XORed with half the row's number, so that eight rows of 8
-            // x 8 blocks fall in different banks.
+            // The warp's 32 columns of a chunk pass through shared memory: z comes
+            // in and the outputs that take its place go out by TMA.  Rows of 64
+            // bytes under the 64-byte swizzle (a row's four 16 bytes XORed with
+            // half the row's number): eight rows of 8 x 8 blocks fall in different
+            // banks.  Where TMA cannot go (z not 16-byte aligned, the rows of a
+            // sequence's last chunk), lane = row lane / 4 of eight, 16 bytes lane % 4.
             const int r8 = lane >> 2, mine = r8 * 64 + (((lane & 3) ^ ((r8 >> 1) & 3)) << 4);
-            const size_t col = (size_t)hv * dv + 32 * (warp & 3) + 8 * (lane & 3);
+            const int wq = warp & 3, col0 = hv * dv + 32 * wq;
+            const size_t col = (size_t)col0 + 8 * (lane & 3);
             const size_t ldo = (size_t)a.HV * dv;
             const uint16_t *z = static_cast<const uint16_t *>(a.z) + (row0 + r8) * a.ldz + col;
             uint16_t *out = static_cast<uint16_t *>(a.out) + (row0 + r8) * ldo + col;
-            const bool zvec = (((uintptr_t)a.z | (uintptr_t)(a.ldz * 2)) & 15u) == 0;
-            unsigned char *so = smem + kOut + (warp & 3) * 4096;
+            unsigned char *so = smem + kOut + wq * 4096;
             const bool gated = a.z != nullptr && on;
             // this lane's row of the 8 x 8 blocks (tokens, columns) of two loads or stores:
             // matrices 0 and 1 are adjacent columns, 2 and 3 the next eight tokens
             const int xr = (lane & 7) >> 1;
             const uint32_t blk = smem_u32(so) + ((lane >> 4) * 8 + (lane & 7)) * 64;
-            // z of a chunk into shared memory, asynchronously where it is 16-byte
-            // aligned; the outputs take its place
+            int armed = -1;
             auto fetch = [&](int c) {
-                const int L = rows_in(c);
-                const uint16_t *q = z + (long long)c * kC * a.ldz;
-                unsigned char *sz = so + (c & 1) * 16384 + mine;
-                if (zvec) {
-#pragma unroll 2
-                    for (int k = 0; k < 8; ++k, q += 8 * a.ldz)
-                        if (8 * k + r8 < L) cp_async16(sz + 512 * k, q);
+                unsigned char *sz = so + (c & 1) * 16384;
+                if (a.z_tma) {
+                    if (lane == 0) {
+                        bulk_wait_read_all();  // the outputs that were there have gone
+                        uint64_t *bar = &bars[ZFULL + 4 * (c & 1) + wq];
+                        mbar_arrive_expect_tx(bar, 4096);
+                        tma_load_2d(sz, &maps.z, col0, (int)(row0 + c * kC), bar);
+                    }
+                    armed = c;
                 } else {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+                    const int L = rows_in(c);
+                    const uint16_t *q = z + (long long)c * kC * a.ldz;
 #pragma unroll 1
                     for (int k = 0; k < 64; ++k) {
                         const int r = k & 56;  // eight rows at a time, element k & 7
                         if (r + r8 < L)
-                            *reinterpret_cast<uint16_t *>(sz + 64 * r + 2 * (k & 7)) =
+                            *reinterpret_cast<uint16_t *>(sz + mine + 64 * r + 2 * (k & 7)) =
                                 __ldg(q + r * a.ldz + (k & 7));
                     }
+                    __syncwarp();
                 }
-                cp_async_commit();
             };
             if (gated && NC > 0) fetch(0);
             uint32_t beyond = 0;  // chunks beyond r's range so far
             for (int c = 0; c < NC && !*abort_flag; ++c) {
                 const int L = rows_in(c);
                 const uint32_t ty = tl + kTmY + 64 * (c & 1);
-                if (gated) {
-                    if (c + 1 < NC)
-                        fetch(c + 1);
-                    else
-                        cp_async_commit();
-                }
                 wait(YDONE + (c & 1), c >> 1);
                 tc_fence_after_sync();
                 const float *e = scal(c, kE);
@@ -560,23 +567,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if (gated) {
-                    cp_async_wait_but_one();
-                    __syncwarp();
+                    if (c + 1 < NC) fetch(c + 1);
+                    if (a.z_tma) wait(ZFULL + 4 * (c & 1) + wq, c >> 1);
                     combine(std::true_type{});
-                } else if (on)
+                } else if (on) {
+                    // the outputs of two chunks before have gone
+                    if (lane == 0) bulk_wait_read_but_one();
+                    __syncwarp();
                     combine(std::false_type{});
+                }
                 tc_fence_before_sync();
                 mbar_arrive(&bars[YFREE + (c & 1)]);
                 if (on) {
-                    __syncwarp();
-                    uint16_t *o = out + (size_t)c * kC * ldo;
-#pragma unroll 2
-                    for (int k = 0; k < 8; ++k, o += 8 * ldo)
-                        if (8 * k + r8 < L)
-                            *reinterpret_cast<uint4 *>(o) =
-                                *reinterpret_cast<const uint4 *>(so + (c & 1) * 16384 + 512 * k + mine);
-                    __syncwarp();
+                    const unsigned char *sc = so + (c & 1) * 16384;
+                    if (L == kC) {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&maps.out, sc, col0, (int)(row0 + c * kC));
+                            bulk_commit_group();
+                        }
+                    } else {
+                        __syncwarp();
+                        uint16_t *o = out + (size_t)c * kC * ldo;
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k, o += 8 * ldo)
+                            if (8 * k + r8 < L)
+                                *reinterpret_cast<uint4 *>(o) =
+                                    *reinterpret_cast<const uint4 *>(sc + 512 * k + mine);
+                    }
                 }
+            }
+            if (lane == 0) {
+                bulk_wait_all();
+                if (*abort_flag && armed >= 0)  // a copy in flight lands before the CTA leaves
+                    mbar_wait_bounded(&bars[ZFULL + 4 * (armed & 1) + wq], (armed >> 1) & 1, kWaitNs);
             }
         }
     } else if (warp != kScalars && warp != kIssueState && warp != kIssueY && warp != kLoads) {
@@ -851,14 +876,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, kTmCols);
 }
 
-// x, b or c as [rows][width], rows ld elements apart: boxes of 64 rows of 64
+// A tensor as [rows][width], rows ld elements apart: boxes of 64 rows of
+// `cols`, swizzled over that many bytes.
 bool encode(EncodeTiledFn fn, CUtensorMap *m, const void *p, long long width, long long rows,
-            long long ld) {
+            long long ld, int cols) {
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)cols, 64}, one[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -885,17 +912,20 @@ bool ssm_chunks_supported(const SsmArgs &a) {
            a.ldc % 8 == 0 && a.ldx < (1LL << 38) && a.ldb < (1LL << 38) && a.ldc < (1LL << 38);
 }
 
-cudaError_t launch_ssm_chunks(const SsmArgs &a, int pass, cudaStream_t stream) {
+cudaError_t launch_ssm_chunks(const SsmArgs &given, int pass, cudaStream_t stream) {
     int *err = nullptr;
     cudaError_t e = device_error_word(&err);
     if (e != cudaSuccess) return e;
     const EncodeTiledFn fn = tma_encode_fn(&e);
     if (e != cudaSuccess) return e;
+    SsmArgs a = given;
     const long long rows = a.cu ? a.cu[a.N] : (long long)a.N * a.T;
-    Maps m;
-    if (!encode(fn, &m.x, a.x, (long long)a.HV * a.dv, rows, a.ldx) ||
-        !encode(fn, &m.b, a.b, (long long)a.HK * a.dk, rows, a.ldb) ||
-        !encode(fn, &m.c, a.c, (long long)a.HK * a.dk, rows, a.ldc))
+    const long long wx = (long long)a.HV * a.dv, wb = (long long)a.HK * a.dk;
+    a.z_tma = a.z && ((uintptr_t)a.z & 15u) == 0 && a.ldz % 8 == 0 && a.ldz < (1LL << 38);
+    Maps m = {};
+    if (!encode(fn, &m.x, a.x, wx, rows, a.ldx, 64) || !encode(fn, &m.b, a.b, wb, rows, a.ldb, 64) ||
+        !encode(fn, &m.c, a.c, wb, rows, a.ldc, 64) || !encode(fn, &m.out, a.out, wx, rows, wx, 32) ||
+        (a.z_tma && !encode(fn, &m.z, a.z, wx, rows, a.ldz, 32)))
         return cudaErrorInvalidValue;
     switch (a.dk) {
         case 32: return pass == 0 ? launch<32, 0>(a, m, err, stream)
