@@ -608,22 +608,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= scores: lane = token t of the chunk
         if (OUT) {
             const int sw = warp & 1, t = 32 * sw + lane;
-            // two warps share the columns up to the row's own half: the first half's rows
-            // take 16 each, the second's 32
-            const int g0 = ((warp - kScore0) >> 2) << sw;
+            // 16 columns at a time, up to the row's own half; two warps take turns.  (A row
+            // behind the sequence's end makes outputs that go nowhere.)
+            const int g0 = (warp - kScore0) >> 2;
             const uint32_t tl = tmem + ((uint32_t)(32 * sw) << 16);
             const float D = a.D ? a.D[hv] : 0.f;
             for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
-                const int L = rows_in(c);
                 wait(FULL + at.st, at.ph);
                 wait(GRAM, c);
                 tc_fence_after_sync();
                 if (c >= 2) wait(MFREE + (c & 1), (c >> 1) - 1);
                 unsigned char *m = smem + kM + (c & 1) * 16384 + kmajor_off(t, 0, kC);
-                const bool row = t < L, far = scal(c, kEnd)[2] != 0.f;
+                const bool far = scal(c, kEnd)[2] != 0.f;
                 const float diag = far ? D : scal(c, kDiag)[t], ct = far ? scal(c, kCum)[t] : 0.f;
 #pragma unroll 1
-                for (int g = g0; g < g0 + 1 + sw; ++g) {
+                for (int g = g0; g < 2 * sw + 2; g += 2) {
                     float d[16], w[16];
                     if (!far) {
 #pragma unroll
@@ -640,26 +639,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[e] = fast_exp2(fmaf(sign, q[e], ct)) * scal(c, kStep)[16 * g + e];
                     }
                     tmem_ld16(tl + kTmG + 16 * g, d);
-                    const int mine = row ? t - 16 * g : -1;
+                    if (g >= 2 * sw) {  // the warp's last: G is free again
+                        tc_fence_before_sync();
+                        mbar_arrive(&bars[GFREE]);
+                    }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float f[8];
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 q = mul2(make_float2(d[e], d[e + 1]), make_float2(w[e], w[e + 1]));
+                        d[e] = q.x;
+                        d[e + 1] = q.y;
+                    }
+                    if (g >= 2 * sw) {  // columns of the row's own half
+                        const int mine = t - 16 * g;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float q = d[8 * h + e] * w[8 * h + e];
-                            f[e] = 8 * h + e < mine ? q : 8 * h + e == mine ? q + diag : 0.f;
+                        for (int e = 0; e < 16; ++e) {
+                            if (e == mine) d[e] += diag;
+                            d[e] = e <= mine ? d[e] : 0.f;
                         }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 16; h += 8) {
                         uint4 hi, lo;
-                        pair2(f[0], f[1], hi.x, lo.x);
-                        pair2(f[2], f[3], hi.y, lo.y);
-                        pair2(f[4], f[5], hi.z, lo.z);
-                        pair2(f[6], f[7], hi.w, lo.w);
-                        *reinterpret_cast<uint4 *>(m + 128 * (2 * g + h)) = hi;
-                        *reinterpret_cast<uint4 *>(m + 8192 + 128 * (2 * g + h)) = lo;
+                        pair2(d[h], d[h + 1], hi.x, lo.x);
+                        pair2(d[h + 2], d[h + 3], hi.y, lo.y);
+                        pair2(d[h + 4], d[h + 5], hi.z, lo.z);
+                        pair2(d[h + 6], d[h + 7], hi.w, lo.w);
+                        *reinterpret_cast<uint4 *>(m + 256 * g + 16 * h) = hi;
+                        *reinterpret_cast<uint4 *>(m + 8192 + 256 * g + 16 * h) = lo;
                     }
                 }
-                tc_fence_before_sync();
-                mbar_arrive(&bars[GFREE]);
                 fence_async_smem();
                 mbar_arrive(&bars[MFULL + (c & 1)]);
             }
