@@ -71,7 +71,7 @@ template <typename T, int W, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads)
     gdr_short_conv_kernel(const T *__restrict__ x, const float *__restrict__ w,
                           const float *__restrict__ bias, const T *s0, T *__restrict__ out, T *st,
-                          int D, long long ldx, long long ldo, int rows,
+                          int D, long long ldx, long long ldo, int rows, bool w16,
                           const __grid_constant__ SeqTable table) {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
@@ -101,8 +101,17 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < W - 1; ++j) V::unpack(before[j], win[j]);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
+        const float *q = w + (size_t)(c + v) * W;
+        if (W == 4 && w16) {  // a channel's taps at once
+            const float4 t = __ldg(reinterpret_cast<const float4 *>(q));
+            tap[0][v] = t.x;
+            tap[1][v] = t.y;
+            tap[2][v] = t.z;
+            tap[W - 1][v] = t.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) tap[j][v] = __ldg(w + (size_t)(c + v) * W + j);
+            for (int j = 0; j < W; ++j) tap[j][v] = __ldg(q + j);
+        }
         b[v] = bias ? __ldg(bias + c + v) : 0.f;
     }
     // the new state: written by the thread that has read the old one, which it may replace
@@ -182,7 +191,8 @@ cudaError_t launch(const ConvArgs &a, int rows, cudaStream_t stream) {
         trace_begin(kKernShortConv, stream);
         gdr_short_conv_kernel<T, W, VEC, SILU><<<dim3((unsigned)units, ny), kThreads, 0, stream>>>(
             static_cast<const T *>(a.x), a.w, a.bias, static_cast<const T *>(a.s0),
-            static_cast<T *>(a.out), static_cast<T *>(a.st), a.D, a.ldx, a.ldo, rows, t);
+            static_cast<T *>(a.out), static_cast<T *>(a.st), a.D, a.ldx, a.ldo, rows,
+            aligned16(a.w), t);
         trace_end(kKernShortConv, stream);
         return cudaGetLastError();
     });

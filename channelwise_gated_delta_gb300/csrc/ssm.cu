@@ -14,10 +14,14 @@
 #include <stdint.h>
 
 #include "gdr.h"
+#include "sm100_ptx.cuh"
 #include "ssm.cuh"
 
 namespace gdr {
 namespace {
+
+using sm100::fma2;
+using sm100::mul2;
 
 constexpr int kTok = 16;
 constexpr int kThreads = 128;
@@ -41,22 +45,21 @@ __global__ void __launch_bounds__(kThreads)
     const int col = tile * kCols + lane;
     const size_t per = (size_t)DK * a.dv;
 
-    float S[R];
+    float2 S[R / 2];  // rows 2 i and 2 i + 1 of the warp's, two operations at a time
     const size_t at = (size_t)(warp * R) * a.dv + col;
 #pragma unroll
-    for (int r = 0; r < R; ++r) S[r] = 0.f;
-    if (a.h0 && u.unit == 0) {
-        const float *h = a.h0 + ((size_t)u.seq * a.HV + hv) * per + at;
+    for (int i = 0; i < R / 2; ++i) S[i] = make_float2(0.f, 0.f);
+    auto rows = [&](const float *p, float keep) {  // S <- keep S + what stands at p
 #pragma unroll
-            for (int r = 0; r < R; ++r) S[r] = h[(size_t)r * a.dv];
-    }
+        for (int i = 0; i < R / 2; ++i)
+            S[i] = fma2(make_float2(keep, keep), S[i],
+                        make_float2(p[(size_t)(2 * i) * a.dv], p[(size_t)(2 * i + 1) * a.dv]));
+    };
+    if (a.h0 && u.unit == 0) rows(a.h0 + ((size_t)u.seq * a.HV + hv) * per + at, 0.f);
     if (PASS == 2)
         for (int i = 0; i < u.unit; ++i) {
             const size_t s = (size_t)(unit - u.unit + i) * a.HV + hv;
-            const float keep = expf(a.seg_log[s]);
-            const float *e = a.seg_state + s * per + at;
-#pragma unroll
-            for (int r = 0; r < R; ++r) S[r] = fmaf(keep, S[r], e[(size_t)r * a.dv]);
+            rows(a.seg_state + s * per + at, expf(a.seg_log[s]));
         }
 
     const T *x = static_cast<const T *>(a.x) + u.row0 * a.ldx + (size_t)hv * a.dv + tile * kCols;
@@ -106,23 +109,20 @@ __global__ void __launch_bounds__(kThreads)
         for (int k = 0; k < n; ++k) {
             const float keep = sdec[k], xs = sstep[k] * sx[k][lane];
             if (PASS == 1) total += slog[k];
-            float y0 = 0.f, y1 = 0.f;
+            const float2 keep2 = make_float2(keep, keep), xs2 = make_float2(xs, xs);
+            float2 y0 = make_float2(0.f, 0.f), y1 = y0;
 #pragma unroll
             for (int r = 0; r < R; r += 4) {
                 const float4 bv = *reinterpret_cast<const float4 *>(&sb[k][warp * R + r]);
-                S[r] = fmaf(keep, S[r], bv.x * xs);
-                S[r + 1] = fmaf(keep, S[r + 1], bv.y * xs);
-                S[r + 2] = fmaf(keep, S[r + 2], bv.z * xs);
-                S[r + 3] = fmaf(keep, S[r + 3], bv.w * xs);
+                S[r / 2] = fma2(keep2, S[r / 2], mul2(make_float2(bv.x, bv.y), xs2));
+                S[r / 2 + 1] = fma2(keep2, S[r / 2 + 1], mul2(make_float2(bv.z, bv.w), xs2));
                 if (PASS != 1) {
                     const float4 cv = *reinterpret_cast<const float4 *>(&sc[k][warp * R + r]);
-                    y0 = fmaf(cv.x, S[r], y0);
-                    y1 = fmaf(cv.y, S[r + 1], y1);
-                    y0 = fmaf(cv.z, S[r + 2], y0);
-                    y1 = fmaf(cv.w, S[r + 3], y1);
+                    y0 = fma2(make_float2(cv.x, cv.y), S[r / 2], y0);
+                    y1 = fma2(make_float2(cv.z, cv.w), S[r / 2 + 1], y1);
                 }
             }
-            if (PASS != 1) part[warp][k][lane] = y0 + y1;
+            if (PASS != 1) part[warp][k][lane] = (y0.x + y0.y) + (y1.x + y1.y);
         }
         __syncthreads();
         if (PASS != 1) {
@@ -150,7 +150,10 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (end)
 #pragma unroll
-        for (int r = 0; r < R; ++r) end[at + (size_t)r * a.dv] = S[r];
+        for (int i = 0; i < R / 2; ++i) {
+            end[at + (size_t)(2 * i) * a.dv] = S[i].x;
+            end[at + (size_t)(2 * i + 1) * a.dv] = S[i].y;
+        }
 }
 
 // Sequences of one token (or none): one CTA per (sequence, value head) passes
