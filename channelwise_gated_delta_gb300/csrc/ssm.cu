@@ -4,12 +4,14 @@
 //     out = S^T c + D x, times silu(z).
 //
 // gdr_ssm_walk_kernel runs it token by token, in float32 throughout, for
-// every type and size.  One CTA per (unit of a sequence, value head, 32
+// every type and size.  One CTA per (unit of a sequence, value head, 32 or 64
 // columns); warp w holds the rows w dk / 4 .. of the columns of its lanes in
-// registers, so that a token is three operations an element of the state and
-// no exchange: the four warps' partial outputs meet in shared memory once
-// every kTok tokens.  A single token is one pass over the state, bound by
-// memory; a long walk is bound by its operations.
+// registers, so that a token is three operations an element of the state (two
+// elements at a time) and no exchange: the four warps' partial outputs meet in
+// shared memory once every kTok tokens.  It is bound by those operations and
+// the loads of b and c from shared memory that feed them.
+// gdr_ssm_step_kernel is one pass over the states of single tokens, bound by
+// memory; bf16 sequences take the chunks of ssm_tc.cu.
 #include <limits.h>
 #include <stdint.h>
 
@@ -25,12 +27,13 @@ using sm100::mul2;
 
 constexpr int kTok = 16;
 constexpr int kThreads = 128;
-constexpr int kCols = 32;
+constexpr int kWideSms = 152;
 
-template <typename T, int DK, int PASS>
+template <typename T, int DK, int PASS, int COLS>
 __global__ void __launch_bounds__(kThreads)
     gdr_ssm_walk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SeqTable table) {
-    constexpr int R = DK / 4;  // rows of a warp
+    constexpr int R = DK / 4;          // rows of a warp
+    constexpr int kCols = 32 * COLS;   // columns of the CTA, a lane's 32 apart
     __shared__ __align__(16) float sb[kTok][DK], sc[kTok][DK];
     __shared__ float sx[kTok][kCols], part[4][kTok][kCols], sstep[kTok], sdec[kTok], slog[kTok];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -42,18 +45,22 @@ __global__ void __launch_bounds__(kThreads)
     const long long cut = a.seg_rows;
     const int t0 = (int)(u.unit * cut), t1 = (int)min((long long)u.len, t0 + cut);
     if (PASS == 1 && t1 == u.len) return;  // no unit follows
-    const int col = tile * kCols + lane;
     const size_t per = (size_t)DK * a.dv;
 
-    float2 S[R / 2];  // rows 2 i and 2 i + 1 of the warp's, two operations at a time
-    const size_t at = (size_t)(warp * R) * a.dv + col;
+    float2 S[COLS][R / 2];  // rows 2 i and 2 i + 1 of the warp's, two operations at a time
+    const size_t at = (size_t)(warp * R) * a.dv + tile * kCols + lane;
 #pragma unroll
-    for (int i = 0; i < R / 2; ++i) S[i] = make_float2(0.f, 0.f);
+    for (int j = 0; j < COLS; ++j)
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i) S[j][i] = make_float2(0.f, 0.f);
     auto rows = [&](const float *p, float keep) {  // S <- keep S + what stands at p
 #pragma unroll
-        for (int i = 0; i < R / 2; ++i)
-            S[i] = fma2(make_float2(keep, keep), S[i],
-                        make_float2(p[(size_t)(2 * i) * a.dv], p[(size_t)(2 * i + 1) * a.dv]));
+        for (int j = 0; j < COLS; ++j)
+#pragma unroll
+            for (int i = 0; i < R / 2; ++i)
+                S[j][i] = fma2(make_float2(keep, keep), S[j][i],
+                               make_float2(p[(size_t)(2 * i) * a.dv + 32 * j],
+                                           p[(size_t)(2 * i + 1) * a.dv + 32 * j]));
     };
     if (a.h0 && u.unit == 0) rows(a.h0 + ((size_t)u.seq * a.HV + hv) * per + at, 0.f);
     if (PASS == 2)
@@ -81,8 +88,8 @@ __global__ void __launch_bounds__(kThreads)
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const int k = (tid + kThreads * i) / kCols;
-            rx[i] = t + k < t1 ? to_f32(x[(t + k) * a.ldx + lane]) : 0.f;
+            const int e = tid + kThreads * i, k = e / kCols;
+            rx[i] = t + k < t1 ? to_f32(x[(t + k) * a.ldx + e % kCols]) : 0.f;
         }
         if (tid < kTok && t + tid < t1) rdt = dt[(long long)(t + tid) * a.HV];
     };
@@ -95,7 +102,10 @@ __global__ void __launch_bounds__(kThreads)
             sc[e / DK][e % DK] = rc[i];
         }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) sx[(tid + kThreads * i) / kCols][lane] = rx[i];
+        for (int i = 0; i < NX; ++i) {
+            const int e = tid + kThreads * i;
+            sx[e / kCols][e % kCols] = rx[i];
+        }
         if (tid < kTok) {
             const float step = t + tid < t1 ? ssm_step(rdt, bias, a.softplus) : 0.f;
             sstep[tid] = step;
@@ -107,33 +117,46 @@ __global__ void __launch_bounds__(kThreads)
         const int n = min(kTok, t1 - t);
 #pragma unroll 2
         for (int k = 0; k < n; ++k) {
-            const float keep = sdec[k], xs = sstep[k] * sx[k][lane];
+            const float keep = sdec[k];
             if (PASS == 1) total += slog[k];
-            const float2 keep2 = make_float2(keep, keep), xs2 = make_float2(xs, xs);
-            float2 y0 = make_float2(0.f, 0.f), y1 = y0;
+            const float2 keep2 = make_float2(keep, keep);
+            float2 xs[COLS], y[COLS], z[COLS];
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) {
+                const float q = sstep[k] * sx[k][lane + 32 * j];
+                xs[j] = make_float2(q, q);
+                y[j] = z[j] = make_float2(0.f, 0.f);
+            }
 #pragma unroll
             for (int r = 0; r < R; r += 4) {
                 const float4 bv = *reinterpret_cast<const float4 *>(&sb[k][warp * R + r]);
-                S[r / 2] = fma2(keep2, S[r / 2], mul2(make_float2(bv.x, bv.y), xs2));
-                S[r / 2 + 1] = fma2(keep2, S[r / 2 + 1], mul2(make_float2(bv.z, bv.w), xs2));
-                if (PASS != 1) {
-                    const float4 cv = *reinterpret_cast<const float4 *>(&sc[k][warp * R + r]);
-                    y0 = fma2(make_float2(cv.x, cv.y), S[r / 2], y0);
-                    y1 = fma2(make_float2(cv.z, cv.w), S[r / 2 + 1], y1);
+                float4 cv = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (PASS != 1) cv = *reinterpret_cast<const float4 *>(&sc[k][warp * R + r]);
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) {
+                    float2 &s0 = S[j][r / 2], &s1 = S[j][r / 2 + 1];
+                    s0 = fma2(keep2, s0, mul2(make_float2(bv.x, bv.y), xs[j]));
+                    s1 = fma2(keep2, s1, mul2(make_float2(bv.z, bv.w), xs[j]));
+                    if (PASS != 1) {
+                        y[j] = fma2(make_float2(cv.x, cv.y), s0, y[j]);
+                        z[j] = fma2(make_float2(cv.z, cv.w), s1, z[j]);
+                    }
                 }
             }
-            if (PASS != 1) part[warp][k][lane] = (y0.x + y0.y) + (y1.x + y1.y);
+            if (PASS != 1)
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) part[warp][k][lane + 32 * j] = (y[j].x + y[j].y) + (z[j].x + z[j].y);
         }
         __syncthreads();
         if (PASS != 1) {
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
-                const int k = (tid + kThreads * i) / kCols;
+                const int e = tid + kThreads * i, k = e / kCols, col = e % kCols;
                 if (k >= n) continue;
-                float y = (part[0][k][lane] + part[1][k][lane]) + (part[2][k][lane] + part[3][k][lane]);
-                y = fmaf(D, sx[k][lane], y);
+                float y = (part[0][k][col] + part[1][k][col]) + (part[2][k][col] + part[3][k][col]);
+                y = fmaf(D, sx[k][col], y);
                 const size_t row = (size_t)(u.row0 + t + k);
-                const size_t o = (size_t)hv * a.dv + col;
+                const size_t o = (size_t)hv * a.dv + tile * kCols + col;
                 if (a.z) y = ssm_gate(y, to_f32(static_cast<const T *>(a.z)[row * a.ldz + o]));
                 static_cast<T *>(a.out)[row * a.HV * a.dv + o] = from_f32<T>(y);
             }
@@ -150,10 +173,12 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (end)
 #pragma unroll
-        for (int i = 0; i < R / 2; ++i) {
-            end[at + (size_t)(2 * i) * a.dv] = S[i].x;
-            end[at + (size_t)(2 * i + 1) * a.dv] = S[i].y;
-        }
+        for (int j = 0; j < COLS; ++j)
+#pragma unroll
+            for (int i = 0; i < R / 2; ++i) {
+                end[at + (size_t)(2 * i) * a.dv + 32 * j] = S[j][i].x;
+                end[at + (size_t)(2 * i + 1) * a.dv + 32 * j] = S[j][i].y;
+            }
 }
 
 // Sequences of one token (or none): one CTA per (sequence, value head) passes
@@ -250,16 +275,25 @@ cudaError_t step_by_dk(const SsmArgs &a, cudaStream_t s) {
                       : a.dk == 64 ? step_by_dv<T, 64>(a, s) : step_by_dv<T, 128>(a, s);
 }
 
-template <typename T, int DK, int PASS>
-cudaError_t launch_walk(const SsmArgs &a, cudaStream_t stream) {
+template <typename T, int DK, int PASS, int COLS>
+cudaError_t launch_cols(const SsmArgs &a, cudaStream_t stream) {
     return for_sequences(a.cu, a.N, a.T, a.seg_rows, [&](const SeqTable &t, long long units) {
-        const long long ctas = units * a.HV * (a.dv / kCols);
+        const long long ctas = units * a.HV * (a.dv / (32 * COLS));
         if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         trace_begin(kKernSsm, stream);
-        gdr_ssm_walk_kernel<T, DK, PASS><<<(unsigned)ctas, kThreads, 0, stream>>>(a, t);
+        gdr_ssm_walk_kernel<T, DK, PASS, COLS><<<(unsigned)ctas, kThreads, 0, stream>>>(a, t);
         trace_end(kKernSsm, stream);
         return cudaGetLastError();
     });
+}
+// Two columns a lane read each row of b and c half as often: f32, 4 x 1024
+// tokens of 32 heads of 128 x 128, 377 us against 458.  Below a CTA for each of
+// kWideSms SMs the narrow ones are twice as many and no slower each.
+template <typename T, int DK, int PASS>
+cudaError_t launch_walk(const SsmArgs &a, cudaStream_t stream) {
+    const long long wide = count_units(a.cu, a.N, a.T, a.seg_rows) * a.HV * (a.dv / 64);
+    return a.dv % 64 == 0 && wide >= kWideSms ? launch_cols<T, DK, PASS, 2>(a, stream)
+                                              : launch_cols<T, DK, PASS, 1>(a, stream);
 }
 template <typename T, int DK>
 cudaError_t by_pass(const SsmArgs &a, int pass, cudaStream_t s) {
