@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads)
                                         make_float2(win[j][v], win[j][v + 1]), q);
                     q = sm100::fma2(make_float2(tap[W - 1][v], tap[W - 1][v + 1]),
                                     make_float2(f[v], f[v + 1]), q);
+                    if (SILU) q = sm100::silu2(q);
                     y[v] = q.x;
                     y[v + 1] = q.y;
                 }
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads)
             }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                if (SILU) y[v] = sm100::silu(y[v]);
+                if (SILU && VEC % 2) y[v] = sm100::silu(y[v]);
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
                 win[W - 2][v] = f[v];

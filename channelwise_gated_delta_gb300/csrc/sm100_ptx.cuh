@@ -242,6 +242,13 @@ __device__ __forceinline__ float silu(float y) {
     return y * fast_rcp(1.f + fast_exp2(-1.4426950408889634f * y));
 }
 
+__device__ __forceinline__ float2 silu2(float2 y) {
+    constexpr float k = -1.4426950408889634f;
+    const float2 e = mul2(y, make_float2(k, k));
+    const float2 q = make_float2(1.f + fast_exp2(e.x), 1.f + fast_exp2(e.y));
+    return mul2(y, make_float2(fast_rcp(q.x), fast_rcp(q.y)));
+}
+
 // ---- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)

@@ -378,6 +378,22 @@ Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, int dtype, u
     return p;
 }
 
+// Whether bf16 sequences are so short that walking them token by token is
+// faster than chunks, by what both cost (microseconds): a CTA of the chunk
+// kernel 8 for itself and 1.4 a chunk, one an SM; the walk its operations at 20
+// TFLOP/s and its states at memory's rate.  64 sequences of 32 heads of 128 x
+// 128: chunks 128 (2 to 16 tokens), walk 97 (2), 110 (4), 137 (8), 173 (16); of
+// 64 x 64, 16 tokens: chunks 90, walk 37.
+bool walk_is_faster(const SsmArgs &a, const Plan &plan) {
+    const int sms = sm_count();
+    if (sms == 0) return false;
+    const double rows = a.cu ? a.cu[a.N] : (double)a.N * a.T, state = (double)a.dk * a.dv;
+    const double waves = (double)((plan.units * a.HV + sms - 1) / sms);
+    const double chunks = waves * (8.0 + 1.4 * (rows / 64 / plan.units < 1 ? 1 : rows / 64 / plan.units));
+    const double walk = rows * a.HV * 5 * state / 20e6 + a.N * a.HV * state * 8 / 6e6 + 0.2 * plan.longest;
+    return walk < chunks;
+}
+
 gdr_status check_shape(const int *cu, int N, int T, int HK, int HV, int dk, int dv, int dtype,
                        unsigned flags) {
     if (N < 0 || (!cu && T < 0) || HK <= 0 || HV <= 0 || HV % HK) return GDR_ERR_SHAPE;
@@ -451,8 +467,9 @@ extern "C" GDR_API gdr_status gdr_ssm_forward(
     SsmArgs a = {x, b, c, z, dt, A, D, dt_bias, h0, out, ht, nullptr, nullptr, ldx, ldb, ldc, ldz,
                  N, T, HK, HV, dk, dv, cu_seqlens, plan.seg_rows,
                  (flags & GDR_FLAG_DT_SOFTPLUS) ? 1 : 0, dtype == GDR_BF16 ? 1 : 0, 0};
-    const auto walk = !(flags & GDR_FLAG_FORCE_GENERIC) && ssm_chunks_supported(a) ? launch_ssm_chunks
-                                                                                   : launch_ssm_walk;
+    const bool chunks = !(flags & GDR_FLAG_FORCE_GENERIC) && ssm_chunks_supported(a) &&
+                        (plan.bytes || !walk_is_faster(a, plan));
+    const auto walk = chunks ? launch_ssm_chunks : launch_ssm_walk;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = cudaSuccess;
     if (plan.bytes) {

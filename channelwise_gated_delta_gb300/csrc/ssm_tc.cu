@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ldsm4_t(at + 1024, *reinterpret_cast<uint32_t (*)[4]>(zt + 4));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                f[i].x *= silu(__uint_as_float(zt[i] << 16));
-                                f[i].y *= silu(__uint_as_float(zt[i] & 0xffff0000u));
+                                f[i] = mul2(f[i], silu2(make_float2(__uint_as_float(zt[i] << 16),
+                                                                    __uint_as_float(zt[i] & 0xffff0000u))));
                             }
                         }
                         tmem_ld_wait(y);
