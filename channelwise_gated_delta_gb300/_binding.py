@@ -585,19 +585,21 @@ def _rows_of(name, t, shape, lead, wide, dtype, index):
     """The distance in elements of the rows of ``t``, ``wide`` elements each, whose indices are the
     first ``lead`` of ``shape``: a ``dtype`` tensor on CUDA device ``index`` whose rows may lie
     further apart than they are wide."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index >= 0:
+        return wide
     if t.get_device() != index or index < 0:
         raise ValueError("%s must be a CUDA tensor%s"
                          % (name, " on cuda:%d" % index if index >= 0 else ""))
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError("%s must be %s %s, got %s %s"
                          % (name, dtype, list(shape), t.dtype, list(t.shape)))
-    if t.is_contiguous():
-        return wide
     strides, want = t.stride(), 1
     for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] != 1 and strides[i] != want:
             raise ValueError("%s must have rows of adjacent elements" % name)
         want *= shape[i]
+    if t.is_contiguous():
+        return wide
     ld = wide
     if shape[lead - 1] != 1:
         ld = strides[lead - 1]
@@ -624,9 +626,11 @@ def _sequences(shape, lead, cu_seqlens):
     return cu, n, 0
 
 
-def _optional(name, t, shape, index):
-    """The address of a float32 tensor of this shape."""
-    _given(name, t, shape, torch.float32, index)
+def _checked(name, t, shape, dtype, index):
+    """The address of a tensor that _given takes, in one comparison where it is right."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index >= 0:
+        return t.data_ptr()
+    _given(name, t, shape, dtype, index)
     return t.data_ptr()
 
 
@@ -641,36 +645,40 @@ def gdr_short_conv(x, weight, bias=None, cu_seqlens=None, s0=None, out=None, st=
     the new state.  ``silu``: out = y / (1 + exp(-y)).  Returns (out, st), allocated when not given.
     """
     lib = load_library()
-    shape = x.shape
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
     lead = len(shape) - 1
     if not 1 <= lead <= 2 or weight.dim() != 2:
         raise ValueError("x must be [B, T, D] or [rows, D] and weight [D, W]")
-    dtype, D, index = x.dtype, shape[lead], x.get_device()
-    code = _dtype_code(dtype, "x")
-    ldx = _rows_of("x", x, shape, lead, D, dtype, index)
-    cu, n, T = _sequences(shape, lead, cu_seqlens)
-    W = weight.shape[1]
-    _given("weight", weight, (D, W), torch.float32, index)
-    s0_ptr = st_ptr = None
+    code = GDR_BF16 if dtype is torch.bfloat16 else _dtype_code(dtype, "x")
+    D, W = shape[lead], weight.shape[1]
+    ldx = D if index >= 0 and x.is_contiguous() else _rows_of("x", x, shape, lead, D, dtype, index)
+    if cu_seqlens is None and lead == 2:
+        cu, n, T = None, shape[0], shape[1]
+    else:
+        cu, n, T = _sequences(shape, lead, cu_seqlens)
+    w_ptr = _checked("weight", weight, (D, W), torch.float32, index)
+    bias_ptr = s0_ptr = st_ptr = None
+    if bias is not None:
+        bias_ptr = _checked("bias", bias, (D,), torch.float32, index)
     if s0 is not None:
-        _given("s0", s0, (n, W - 1, D), dtype, index)
-        s0_ptr = s0.data_ptr()
-    ldo = D if out is None else _rows_of("out", out, shape, lead, D, dtype, index)
-    if st is not None and st is not s0:
-        _given("st", st, (n, W - 1, D), dtype, index)
+        s0_ptr = _checked("s0", s0, (n, W - 1, D), dtype, index)
+    ldo = D
+    if out is not None:
+        ldo = _rows_of("out", out, shape, lead, D, dtype, index)
+    if st is not None:
+        st_ptr = s0_ptr if st is s0 else _checked("st", st, (n, W - 1, D), dtype, index)
     if out is None or (st is None and store_st):
         with _memory_of(stream):
             if out is None:
-                out = torch.empty(shape, dtype=dtype, device=x.device)
+                out = torch.empty_like(x) if ldx == D else torch.empty(shape, dtype=dtype,
+                                                                       device=x.device)
             if st is None and store_st:
                 st = (torch.empty_like(s0) if s0 is not None else
                       torch.empty((n, max(W - 1, 0), D), dtype=dtype, device=x.device))
-    if st is not None:
-        st_ptr = st.data_ptr()
+                st_ptr = st.data_ptr()
     status = _on(index, lib.gdr_short_conv)(
-        x.data_ptr(), weight.data_ptr(), None if bias is None else _optional("bias", bias, (D,), index),
-        s0_ptr, out.data_ptr(), st_ptr, cu, n, T, D, W, ldx, ldo, _stream_of(stream, index), code,
-        GDR_FLAG_SILU if silu else 0)
+        x.data_ptr(), w_ptr, bias_ptr, s0_ptr, out.data_ptr(), st_ptr, cu, n, T, D, W, ldx, ldo,
+        _stream_of(stream, index), code, GDR_FLAG_SILU if silu else 0)
     if status != GDR_OK:
         _check(lib, status)
     return out, st
@@ -700,50 +708,54 @@ def gdr_qk_norm(q, k, weight_q=None, weight_k=None, positions=None, freqs=None, 
     rotated, as pairs (i, i + half), or neighbours if ``interleaved``.  ``out_q=q`` and
     ``out_k=k`` work in place.  Returns (out_q, out_k), allocated when not given."""
     lib = load_library()
-    shape, kshape = q.shape, k.shape
+    shape, kshape, dtype, index = q.shape, k.shape, q.dtype, q.get_device()
     lead = len(shape) - 2
     if not 1 <= lead <= 2 or len(kshape) != lead + 2:
         raise ValueError("q and k must be [B, T, H, d] or [rows, H, d]")
     if norm != "l2" and norm != "rms":
         raise ValueError('norm must be "l2" or "rms"')
-    dtype, index = q.dtype, q.get_device()
+    code = GDR_BF16 if dtype is torch.bfloat16 else _dtype_code(dtype, "q and k")
     HQ, d, HK = shape[lead], shape[lead + 1], kshape[lead]
-    code = _dtype_code(dtype, "q and k")
     rows = shape[0] if lead == 1 else shape[0] * shape[1]
     if kshape[:lead] != shape[:lead] or kshape[lead + 1] != d:
         raise ValueError("k must match q in rows and d")
-    ldq = _rows_of("q", q, shape, lead, HQ * d, dtype, index)
-    ldk = _rows_of("k", k, kshape, lead, HK * d, dtype, index)
-    d_rot, pos_ptr, freq_ptr = 0, None, None
+    wq, wk = HQ * d, HK * d
+    ldq = _rows_of("q", q, shape, lead, wq, dtype, index)
+    ldk = _rows_of("k", k, kshape, lead, wk, dtype, index)
+    d_rot, pos_ptr, freq_ptr, wq_ptr, wk_ptr = 0, None, None, None, None
     if freqs is not None or positions is not None:
         if freqs is None or positions is None:
             raise ValueError("a rotation needs positions and freqs")
         if freqs.dim() != 1:
             raise ValueError("freqs must be [d_rot / 2]")
-        d_rot = 2 * freqs.shape[0]
-        _given("freqs", freqs, (d_rot // 2,), torch.int64, index)
-        _given("positions", positions, shape[:lead], torch.int32, index)
-        if d_rot:
-            pos_ptr, freq_ptr = positions.data_ptr(), freqs.data_ptr()
-    ldoq, ldok = HQ * d, HK * d
+        half = freqs.shape[0]
+        freq_ptr = _checked("freqs", freqs, (half,), torch.int64, index)
+        pos_ptr = _checked("positions", positions, shape[:lead], torch.int32, index)
+        d_rot = 2 * half
+        if not half:
+            pos_ptr = freq_ptr = None
+    if weight_q is not None:
+        wq_ptr = _checked("weight_q", weight_q, (d,), torch.float32, index)
+    if weight_k is not None:
+        wk_ptr = _checked("weight_k", weight_k, (d,), torch.float32, index)
+    ldoq, ldok = wq, wk
     if out_q is not None:
-        ldoq = ldq if out_q is q else _rows_of("out_q", out_q, shape, lead, HQ * d, dtype, index)
+        ldoq = ldq if out_q is q else _rows_of("out_q", out_q, shape, lead, wq, dtype, index)
     if out_k is not None:
-        ldok = ldk if out_k is k else _rows_of("out_k", out_k, kshape, lead, HK * d, dtype, index)
+        ldok = ldk if out_k is k else _rows_of("out_k", out_k, kshape, lead, wk, dtype, index)
     if out_q is None or out_k is None:
         with _memory_of(stream):
+            device = q.device
             if out_q is None:
-                out_q = torch.empty(shape, dtype=dtype, device=q.device)
+                out_q = torch.empty(shape, dtype=dtype, device=device)
             if out_k is None:
-                out_k = torch.empty(kshape, dtype=dtype, device=q.device)
+                out_k = torch.empty(kshape, dtype=dtype, device=device)
     flags = (GDR_FLAG_RMS_NORM if norm == "rms" else 0) | (
         GDR_FLAG_ROPE_INTERLEAVED if interleaved else 0)
     status = _on(index, lib.gdr_qk_norm)(
-        q.data_ptr(), k.data_ptr(),
-        None if weight_q is None else _optional("weight_q", weight_q, (d,), index),
-        None if weight_k is None else _optional("weight_k", weight_k, (d,), index), pos_ptr, freq_ptr,
-        out_q.data_ptr(), out_k.data_ptr(), rows, HQ, HK, d, d_rot, ldq, ldk, ldoq, ldok, eps,
-        q_scale, _stream_of(stream, index), code, flags)
+        q.data_ptr(), k.data_ptr(), wq_ptr, wk_ptr, pos_ptr, freq_ptr, out_q.data_ptr(),
+        out_k.data_ptr(), rows, HQ, HK, d, d_rot, ldq, ldk, ldoq, ldok, eps, q_scale,
+        _stream_of(stream, index), code, flags)
     if status != GDR_OK:
         _check(lib, status)
     return out_q, out_k
@@ -767,29 +779,35 @@ def gdr_ssm_forward(x, b, c, dt, a, d=None, z=None, dt_bias=None, cu_seqlens=Non
     place of [B, T].  h0, ht [B, HV, dk, dv] f32 as in gdr_forward (``ht=h0`` updates in place;
     ``store_ht=False`` skips it).  d, z, dt_bias, h0 may be None.  Returns (out, ht)."""
     lib = load_library()
-    shape, bshape = x.shape, b.shape
+    shape, bshape, dtype, index = x.shape, b.shape, x.dtype, x.get_device()
     lead = len(shape) - 2
     if not 1 <= lead <= 2 or len(bshape) != lead + 2:
         raise ValueError("x and b must be [B, T, H, d] or [rows, H, d]")
-    dtype, index = x.dtype, x.get_device()
     HV, dv, HK, dk = shape[lead], shape[lead + 1], bshape[lead], bshape[lead + 1]
-    code = _dtype_code(dtype, "x, b and c")
+    code = GDR_BF16 if dtype is torch.bfloat16 else _dtype_code(dtype, "x, b and c")
     if bshape[:lead] != shape[:lead]:
         raise ValueError("b must match x in rows")
-    ldx = _rows_of("x", x, shape, lead, HV * dv, dtype, index)
-    ldb = _rows_of("b", b, bshape, lead, HK * dk, dtype, index)
-    ldc = _rows_of("c", c, bshape, lead, HK * dk, dtype, index)
-    ldz, z_ptr = 0, None
+    wx, wb, f32 = HV * dv, HK * dk, torch.float32
+    ldx = _rows_of("x", x, shape, lead, wx, dtype, index)
+    ldb = _rows_of("b", b, bshape, lead, wb, dtype, index)
+    ldc = _rows_of("c", c, bshape, lead, wb, dtype, index)
+    ldz, z_ptr, d_ptr, bias_ptr, h0_ptr, ht_ptr = 0, None, None, None, None, None
     if z is not None:
-        ldz, z_ptr = _rows_of("z", z, shape, lead, HV * dv, dtype, index), z.data_ptr()
-    _given("dt", dt, shape[:lead + 1], torch.float32, index)
-    _given("a", a, (HV,), torch.float32, index)
-    cu, n, T = _sequences(shape, lead, cu_seqlens)
-    h0_ptr = ht_ptr = None
+        ldz, z_ptr = _rows_of("z", z, shape, lead, wx, dtype, index), z.data_ptr()
+    dt_ptr = _checked("dt", dt, shape[:lead + 1], f32, index)
+    a_ptr = _checked("a", a, (HV,), f32, index)
+    if d is not None:
+        d_ptr = _checked("d", d, (HV,), f32, index)
+    if dt_bias is not None:
+        bias_ptr = _checked("dt_bias", dt_bias, (HV,), f32, index)
+    if cu_seqlens is None and lead == 2:
+        cu, n, T = None, shape[0], shape[1]
+    else:
+        cu, n, T = _sequences(shape, lead, cu_seqlens)
     if h0 is not None:
-        h0_ptr = _optional("h0", h0, (n, HV, dk, dv), index)
-    if ht is not None and ht is not h0:
-        _given("ht", ht, (n, HV, dk, dv), torch.float32, index)
+        h0_ptr = _checked("h0", h0, (n, HV, dk, dv), f32, index)
+    if ht is not None:
+        ht_ptr = h0_ptr if ht is h0 else _checked("ht", ht, (n, HV, dk, dv), f32, index)
     if out is not None:
         _given("out", out, shape, dtype, index)
     if softplus:
@@ -800,22 +818,20 @@ def gdr_ssm_forward(x, b, c, dt, a, d=None, z=None, dt_bias=None, cu_seqlens=Non
     if out is None or (ht is None and store_ht) or need:
         with _memory_of(stream):
             if out is None:
-                out = torch.empty(shape, dtype=dtype, device=x.device)
+                out = torch.empty_like(x) if ldx == wx else torch.empty(shape, dtype=dtype,
+                                                                        device=x.device)
             if ht is None and store_ht:
                 ht = (torch.empty_like(h0) if h0 is not None else
-                      torch.empty((n, HV, dk, dv), dtype=torch.float32, device=x.device))
+                      torch.empty((n, HV, dk, dv), dtype=f32, device=x.device))
+                ht_ptr = ht.data_ptr()
             if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
                 workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     if need:
         if workspace.get_device() != index:
             raise ValueError("workspace must be a CUDA tensor on cuda:%d" % index)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if ht is not None:
-        ht_ptr = ht.data_ptr()
     status = _on(index, lib.gdr_ssm_forward)(
-        x.data_ptr(), b.data_ptr(), c.data_ptr(), dt.data_ptr(), a.data_ptr(),
-        None if d is None else _optional("d", d, (HV,), index), z_ptr,
-        None if dt_bias is None else _optional("dt_bias", dt_bias, (HV,), index), h0_ptr,
+        x.data_ptr(), b.data_ptr(), c.data_ptr(), dt_ptr, a_ptr, d_ptr, z_ptr, bias_ptr, h0_ptr,
         out.data_ptr(), ht_ptr, cu, n, T, HK, HV, dk, dv, ldx, ldb, ldc, ldz,
         _stream_of(stream, index), code, ws_ptr, ws_bytes, flags)
     if status != GDR_OK:
