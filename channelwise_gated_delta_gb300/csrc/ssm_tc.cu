@@ -83,14 +83,16 @@ constexpr uint32_t kScalBytes = 1552;
 constexpr float kRange = 80.f;
 constexpr uint32_t kOut = (kScal + kRing * kScalBytes + 1023) / 1024 * 1024;  // [2][4 warps] [64 t][32]
                                                                               // z, then outputs
-constexpr uint32_t kBars = kOut + 2 * 16384;
+constexpr uint32_t kBad = kOut + 2 * 16384;  // [kRing][128] a column's first token that is not finite
+constexpr uint32_t kBadAt = kBad + kRing * 128;  // [kRing][4 warps] whether there is any
+constexpr uint32_t kBars = kBadAt + kRing * 16;
 enum {
     FULL = 0,               // [3] x, b, c of a chunk in, and its scalars
     EMPTY = FULL + kStages,  // [3] its last product done
     FIX = EMPTY + kStages,   // rows behind the sequence's end zeroed
     GRAM,                    // G done
     GFREE,                   // G read
-    MFULL,                   // [2] M written
+    MFULL,                   // [2] M written, x looked through
     MFREE = MFULL + 2,       // [2] M read
     WX = MFREE + 2,          // [2] (w x)^T written
     WFREE = WX + 2,          // [2] (w x)^T read
@@ -256,6 +258,23 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(p));
     return p != 0;
 }
+// 0 times a value that is not finite is no 0: such values of a column of x are
+// taken out of the tile that Y1 reads, so that they do not reach the outputs of
+// the tokens before them, and the first one's place is kept for the outputs.
+__device__ __noinline__ void mask_odd(unsigned char *smem, int stage, int c, int p) {
+    unsigned char *x = smem + stage * kStage + kX + (p >> 6) * 8192 + (p & 7) * 2;
+    int first = kC;
+    for (int r = kC - 1; r >= 0; --r) {
+        uint16_t *v = reinterpret_cast<uint16_t *>(x + r * 128 + ((((p & 63) >> 3) ^ (r & 7)) << 4));
+        if ((*v & 0x7f80u) == 0x7f80u) {
+            first = r;
+            *v = 0;
+        }
+    }
+    smem[kBad + (c & (kRing - 1)) * 128 + p] = (unsigned char)first;
+    fence_async_smem();
+}
+
 template <int DK, int PASS>
 __global__ void __launch_bounds__(kThreads, 1)
     gdr_ssm_chunk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SeqTable table,
@@ -283,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
-            const int n = i == GFREE || i == MFULL || i == MFULL + 1 || i == WX || i == WX + 1 ||
-                                  i == YFREE || i == YFREE + 1 || i == YSCALED
+            const int n = i == GFREE || i == WX || i == WX + 1 || i == YFREE || i == YFREE + 1 || i == YSCALED
                               ? 128
+                          : i == MFULL || i == MFULL + 1                ? 256
                           : i == DFREE || i == SFULL               ? 4 * DK
                           : i < EMPTY || (i < EMPTY + kStages && OUT) ? 2
                                                                      : 1;
@@ -432,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (on) {
                 const uint2 *w = reinterpret_cast<const uint2 *>(scal(c, kW)) + (lane & 3);
                 const uint32_t tw = tl + kTmW + 64 * (c & 1);
+                uint32_t odd = 0;  // NaN where a value is not finite
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     const int hh = k & 1, s32 = k >> 1;  // half of the columns, of the tokens
@@ -439,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t q[8], h[8], l[8];
                     ldsm4_t(x, *reinterpret_cast<uint32_t (*)[4]>(q));
                     ldsm4_t(x + 2048, *reinterpret_cast<uint32_t (*)[4]>(q + 4));
+                    if (OUT)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(q[j]), "r"(0));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint2 ww = w[16 * s32 + 4 * j];
@@ -450,9 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_16x128(to + 32, l);
                 }
                 tmem_st_wait();
+                if (OUT) {
+                    const bool any = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
+                    if (any) mask_odd(smem, st, c, p0 + lane);
+                    if (lane == 0)
+                        *reinterpret_cast<uint32_t *>(smem + kBadAt + (c & (kRing - 1)) * 16 + (warp & 3) * 4) = any;
+                }
             }
             tc_fence_before_sync();
             mbar_arrive(&bars[WX + (c & 1)]);
+            if (OUT) {
+                if (c >= 2) wait(MFREE + (c & 1), (c >> 1) - 1);
+                mbar_arrive(&bars[MFULL + (c & 1)]);
+            }
         }
     } else if (warp < kScore0) {
         // ================= outputs
@@ -579,7 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 mbar_arrive(&bars[YFREE + (c & 1)]);
                 if (on) {
-                    const unsigned char *sc = so + (c & 1) * 16384;
+                    unsigned char *sc = so + (c & 1) * 16384;
+                    if (*reinterpret_cast<const uint32_t *>(smem + kBadAt + (c & (kRing - 1)) * 16 + wq * 4)) {
+                        // from a value of x on that is not finite
+                        __syncwarp();
+                        for (int r = smem[kBad + (c & (kRing - 1)) * 128 + 32 * wq + lane]; r < kC; ++r)
+                            *reinterpret_cast<uint16_t *>(sc + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                                                          (lane & 7) * 2) = 0x7fff;
+                    }
                     if (L == kC) {
                         fence_async_smem();
                         __syncwarp();
@@ -758,7 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // r a whole number, so that exp(r) S is S but for its exponent
             float r = rintf(0.5f * (all0 + all1));
             const float p0 = before + c0, p1 = before + c1;
-            const bool far = __any_sync(0xffffffffu, fabsf(p0 - r) > kRange || fabsf(p1 - r) > kRange);
+            // (a sum that is not a number counts as beyond: it would reach all of r's chunk)
+            const bool far = __any_sync(0xffffffffu, !(fabsf(p0 - r) <= kRange && fabsf(p1 - r) <= kRange));
             uint2 w;
             pair2(fast_exp2(behind + f0) * s0, fast_exp2(behind + f1) * s1, w.x, w.y);
             *reinterpret_cast<uint2 *>(q + kW / 4) = w;

@@ -604,12 +604,19 @@ GDR_API gdr_status gdr_qk_norm(const void *q, const void *k, const float *weight
  *
  * Sequences, rows and limits as above; HV % HK == 0, dk and dv in {32, 64,
  * 128}.  x, b, c and z aligned to their elements, out, h0 and ht 16-byte, the
- * rest 4-byte.  The state is float32 throughout; an output is rounded once.
+ * rest 4-byte.  The state is float32 throughout and so is an output until it is
+ * rounded; bf16 sequences run by chunks of 64 tokens on the tensor cores (x, b
+ * and c 16-byte aligned, their distances multiples of 16 bytes; otherwise token by
+ * token, as f32 and short ones), where the outputs read a copy of the state
+ * rounded to bf16.  A value that is not finite reaches no output of an earlier
+ * token; from there on its column (x, z) or head comes out as NaN or infinite.
  *
  * `workspace`: device memory of gdr_ssm_workspace_bytes(...) bytes, 256-byte
  * aligned, untouched by anything else until the stream has passed the call;
- * NULL where that is 0.  It is needed where long walks are cut into segments
- * (GDR_FLAG_SEGMENTS(n): into at most n; GDR_FLAG_NO_SEGMENTS: never); the results agree to float32 rounding.
+ * NULL where that is 0.  It is needed where a long sequence of few heads, which
+ * would leave SMs idle, is cut into segments: their end states are formed at once,
+ * then all of them from the states that follow.  GDR_FLAG_SEGMENTS(n): into at
+ * most n; GDR_FLAG_NO_SEGMENTS: never.  The results agree to the route's rounding.
  * GDR_FLAG_FORCE_GENERIC: token by token on CUDA cores whatever the route
  * (for tests).  Errors as gdr_forward_ex.
  */

@@ -175,3 +175,35 @@ def test_runs_are_alike():
         a = gdr_ssm_forward(**d, cu_seqlens=[0, 2000], flags=flags)
         b = gdr_ssm_forward(**d, cu_seqlens=[0, 2000], flags=flags)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype,flags", [("bf16", 0), ("f32", 0), ("bf16", gdr_flag_segments(3))])
+@pytest.mark.parametrize("name", ["x", "b", "c", "dt", "z"])
+def test_values_that_are_not_finite_stay_behind_their_token(dtype, flags, name):
+    """What is not finite reaches no output of a token before it, wherever it stands in a chunk, and
+    none of another column (x, z) or head."""
+    T, HK, HV, D = 200, 1, 3, 128
+    d = draw([T], HK, HV, D, D, dtype, seed=9)
+    clean, _ = gdr_ssm_forward(**d, cu_seqlens=[0, T], flags=flags)
+    for t, v in ((0, "nan"), (5, "inf"), (37, "-inf"), (63, "nan"), (64, "nan"), (100, "inf"), (199, "nan")):
+        e = dict(d, **{name: d[name].clone()})
+        if name == "dt":
+            e["dt"][t, 1] = float(v)
+        else:
+            e[name][t, 0 if name in "bc" else 1, 70] = float(v)
+        out, _ = gdr_ssm_forward(**e, cu_seqlens=[0, T], flags=flags)
+        gdr_device_check()
+        # nothing else than a chunk's own reference may differ: compare by the tolerance of a rounding
+        tol = 4e-2 * clean.float().abs().amax()
+        same = torch.ones(T, HV, D, dtype=torch.bool, device="cuda")
+        if name in "bc":
+            same[t:] = False
+        elif name == "dt":
+            same[t:, 1] = False
+        else:
+            same[t:, 1, 70] = False
+        assert torch.isfinite(out[same].float()).all(), (name, t)
+        assert ((out - clean).float()[same].abs() <= tol).all(), (name, t)
+        if name != "dt" and v == "nan":
+            hit = out[t, :, :] if name in "bc" else out[t, 1, 70]
+            assert not torch.isfinite(hit.float()).any(), (name, t)
