@@ -20,27 +20,37 @@
 //     Y  = S^T c^T          S^T as bf16 in tensor memory
 //     Y += x^T M^T          x as it came (M-major A), M from the score warps
 //     dS = (w x)^T b        (w x)^T in tensor memory, b as it came
-// x, b and c are exact.  M and w x go in as pairs hi + lo of bf16 numbers, off
-// by 2^-16: the state, which is float32 in registers and never rounded
-// itself, keeps float32's accuracy.  The copy of S that Y reads is rounded
+// x, b and c are exact.  w x goes in as three bf16 numbers (see weigh3), off by
+// 8e-7 of it: the state, which is float32 in registers and never rounded itself,
+// keeps float32's accuracy but for that.  (A pair is off by 4e-6, and 406 us
+// where three take 405: the products are not what the kernel waits for.)  M goes
+// in as a pair hi + lo, off by 2^-16.  The copy of S that Y reads is rounded
 // once to bf16: its error is averaged over dk products and adds 1 to 27 % to
 // what the output's own rounding leaves (M rounded the same way would add 26
 // to 48 %).
 //
 // The walk's only serial part is S <- g S + dS in the chain warps: dS does not
-// depend on S and is ready ahead, and Y and w x have two buffers each, so that
-// the products follow one another without waiting for the warps.
-//     0-15   chain: lane = value column, 32 of the dk columns each; S in
+// depend on S.  Tensor memory, full: G 64 columns, Y 2 x 64, S 64, dS 128, w x
+// 96.  So w x has one buffer, in two halves of 32 tokens that are written as
+// soon as the last chunk's products have read them.
+//     0-7    chain: lane = value column, 64 of the dk columns each; S in
 //            registers, its bf16 copy into tensor memory
-//     16-19  (w x)^T into tensor memory
-//     20-23  outputs: Y exp(cum - r), times silu(z)
-//     24, 25, 28, 29  scores: rows of G to rows of M (G's 64 rows are TMEM lanes
+//     8-15   (w x)^T of 32 columns and 32 tokens into tensor memory
+//     16-19  outputs: Y exp(cum - r), times silu(z)
+//     20, 21, 24, 25  scores: rows of G to rows of M (G's 64 rows are TMEM lanes
 //            0-63, which only warps 4 n and 4 n + 1 can read)
-//     26     the chunk's scalars (steps, prefix sums, decays), two tokens a lane
-//     31     TMA of x, b and c, up to three chunks ahead
-//     27, 30 issue the MMAs (one thread each): G and dS; Y.  An MMA takes its
-//            thread as long as the tensor cores (32 to 64 cycles each), and a
-//            thread that waits for one product's inputs feeds no other
+//     22     the chunk's scalars (steps, prefix sums, decays), two tokens a lane
+//     27     TMA of x, b and c, up to three chunks ahead
+//     23, 26 issue the MMAs (one thread each): G and dS; Y.  An MMA takes its
+//            thread as long as the tensor cores (32 to 64 cycles each, some eight
+//            ahead), and a thread that waits for one product's inputs feeds no other
+// The chain's registers (112 a thread) come from the others (56).
+//
+// What bounds it: 4 x 16384 tokens of 32 heads of 128 take 405 us, 3000 cycles a
+// chunk.  Its products take 1790 of them, its bytes 1820 (at 6.8 TB/s).
+// The rest is one chunk's way around: products of dS 770, its read 200, S 600 to
+// 900, the next products' start 200, with the other products in between.  With
+// all arithmetic of the warps taken out it takes 380.
 // Every wait is bounded: a timeout sets the CTA's abort flag and the library's
 // error word, and everyone runs out its loop.
 #include <cuda.h>
@@ -59,10 +69,14 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = 64;
-constexpr int kWarps = 32;
+constexpr int kWarps = 28;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWx0 = 16, kOut0 = 20, kScore0 = 24, kScalars = 26, kIssueState = 27, kIssueY = 30,
-              kLoads = 31;
+constexpr int kWx0 = 8, kOut0 = 16, kScore0 = 20, kScalars = 22, kIssueState = 23, kIssueY = 26,
+              kLoads = 27;
+// registers: 72 a thread at launch, of which the chain's two warpgroups take 112
+// and the others keep 56
+constexpr int kRegsLaunch = 72, kRegsChain = 112, kRegsOther = 56;
+static_assert(2 * kRegsChain + 5 * kRegsOther == 7 * kRegsLaunch && kThreads * kRegsLaunch <= 65536, "registers");
 constexpr int kStages = 3;
 constexpr int kRing = 8;  // chunks whose scalars are held
 // a wait's limit: tries, of some 50 cycles each at least
@@ -75,17 +89,19 @@ constexpr uint32_t kTile = 16384;  // 64 rows of up to 128, two boxes of 64 colu
 constexpr uint32_t kX = 0, kB = kTile, kCm = 2 * kTile, kStage = 3 * kTile;
 constexpr uint32_t kM = kStages * kStage;           // [2] x {hi, lo} [64 t][64 s]
 constexpr uint32_t kScal = kM + 2 * 16384;          // [kRing] of the following
-// of a chunk, 64 numbers each: exp(cum - r), w as pairs {hi, lo} of two tokens,
-// exp(r - cum) step, D exp(r - cum); in a chunk beyond r's range kV the sums
-// behind and kCum up to a token within its half, and the steps; then exp(cum_end), exp(r) and whether the chunk is beyond r's range
-constexpr uint32_t kE = 0, kW = 256, kV = 512, kDiag = 768, kCum = 1024, kStep = 1280, kEnd = 1536;
-constexpr uint32_t kScalBytes = 1552;
+// of a chunk, 64 numbers each: exp(cum - r), exp(r - cum) step, D exp(r - cum);
+// in a chunk beyond r's range kV the sums behind and kCum up to a token within
+// its half, and the steps; of every two tokens w's three parts and a gap; then
+// exp(cum_end), exp(r) and whether the chunk is beyond r's range
+constexpr uint32_t kE = 0, kV = 256, kDiag = 512, kCum = 768, kStep = 1024, kW = 1280, kEnd = 1792;
+constexpr uint32_t kScalBytes = 1808;
 constexpr float kRange = 80.f;
 constexpr uint32_t kOut = (kScal + kRing * kScalBytes + 1023) / 1024 * 1024;  // [2][4 warps] [64 t][32]
                                                                               // z, then outputs
-constexpr uint32_t kBad = kOut + 2 * 16384;  // [kRing][128] a column's first token that is not finite
-constexpr uint32_t kBadAt = kBad + kRing * 128;  // [kRing][4 warps] whether there is any
-constexpr uint32_t kBars = kBadAt + kRing * 16;
+constexpr uint32_t kBad = kOut + 2 * 16384;  // [kRing][2][128] a column's first token, of either half's,
+                                             // that is not finite
+constexpr uint32_t kBadAt = kBad + kRing * 256;  // [kRing][4 x 32 columns][2] whether there is any
+constexpr uint32_t kBars = kBadAt + kRing * 8;
 enum {
     FULL = 0,               // [3] x, b, c of a chunk in, and its scalars
     EMPTY = FULL + kStages,  // [3] its last product done
@@ -94,7 +110,7 @@ enum {
     GFREE,                   // G read
     MFULL,                   // [2] M written, x looked through
     MFREE = MFULL + 2,       // [2] M read
-    WX = MFREE + 2,          // [2] (w x)^T written
+    WX = MFREE + 2,          // [2 x 32 tokens] (w x)^T written
     WFREE = WX + 2,          // [2] (w x)^T read
     DELTA = WFREE + 2,       // dS done
     DFREE,                   // dS read
@@ -143,8 +159,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // Waits for a phase of the barrier; where it has not come in kTries tries (a
 // second or more), sets the CTA's abort flag and goes on: every warp looks at
 // the flag once a chunk.  As few instructions as that takes: the kernel's warps
-// run seven different programs out of one instruction cache, and it ran at 0.65
-// of its speed while their code took 88 KB instead of 60.
+// run eight different programs out of one instruction cache.
 __device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b32 n;\n\t"
@@ -168,18 +183,29 @@ __device__ __forceinline__ void pair2(float a, float b, uint32_t &hi, uint32_t &
                           make_float2(-1.f, -1.f), make_float2(a, b));
     lo = pack2(r.x, r.y);
 }
-// x w of two bf16 numbers x and two weights w = wh + wl (bf16 each) as
-// hi + lo: hi = x wh rounded, whose remainder fits eight bits and so bf16,
-// lo = that remainder + x wl.  Off by 2^-17 of hi.
-__device__ __forceinline__ void weigh2(uint32_t x, uint32_t wh, uint32_t wl, uint32_t &hi,
-                                       uint32_t &lo) {
+// A float32 weight as w0 + w1 + w2: the nearest power of two, and what is left
+// of it as two bf16 numbers.
+__device__ __forceinline__ void split_weight(float w, float &w0, float &w1, float &w2) {
+    w0 = __uint_as_float((__float_as_uint(w) + 0x400000u) & 0xff800000u);
+    const float d = w - w0;
+    w1 = __bfloat162float(__float2bfloat16_rn(d));
+    w2 = d - w1;
+}
+// x w of two bf16 numbers x and their weights as the sum of three bf16 numbers:
+// x w0, which is exact, x w1 rounded, and x w2 with what that rounding left
+// (eight bits, so exact).  The last one's own rounding stays: w0 leaves a
+// third of w at the most, which makes that 8e-7 of x w (rms over weights of any
+// size), where a pair of bf16 numbers leaves 4e-6 of it and three parts of the
+// float32 product, exact, take eleven instructions in place of four.
+__device__ __forceinline__ void weigh3(uint32_t x, uint4 w, uint32_t &q0, uint32_t &q1, uint32_t &q2) {
     asm("{\n\t.reg .b32 n, r;\n\t"
-        "mul.rn.bf16x2 %0, %2, %3;\n\t"
-        "neg.bf16x2 n, %0;\n\t"
-        "fma.rn.bf16x2 r, %2, %3, n;\n\t"
-        "fma.rn.bf16x2 %1, %2, %4, r;\n\t}"
-        : "=&r"(hi), "=r"(lo)
-        : "r"(x), "r"(wh), "r"(wl));
+        "mul.rn.bf16x2 %0, %3, %4;\n\t"
+        "mul.rn.bf16x2 %1, %3, %5;\n\t"
+        "neg.bf16x2 n, %1;\n\t"
+        "fma.rn.bf16x2 r, %3, %5, n;\n\t"
+        "fma.rn.bf16x2 %2, %3, %6, r;\n\t}"
+        : "=&r"(q0), "=&r"(q1), "=r"(q2)
+        : "r"(x), "r"(w.x), "r"(w.y), "r"(w.z));
 }
 
 // Four 8 x 8 matrices of 16-bit numbers between shared memory and registers,
@@ -259,20 +285,30 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 // 0 times a value that is not finite is no 0: such values of a column of x are
-// taken out of the tile that Y1 reads, so that they do not reach the outputs of
-// the tokens before them, and the first one's place is kept for the outputs.
-__device__ __noinline__ void mask_odd(unsigned char *smem, int stage, int c, int p) {
+// taken out of the tile that Y1 reads (of its rows r0 to r0 + 31), so that they
+// do not reach the outputs of the tokens before them, and the first one's place
+// is kept for the outputs.
+__device__ __noinline__ void mask_odd(unsigned char *smem, int stage, int r0, unsigned char *bad, int p) {
     unsigned char *x = smem + stage * kStage + kX + (p >> 6) * 8192 + (p & 7) * 2;
     int first = kC;
-    for (int r = kC - 1; r >= 0; --r) {
+    for (int r = r0 + 31; r >= r0; --r) {
         uint16_t *v = reinterpret_cast<uint16_t *>(x + r * 128 + ((((p & 63) >> 3) ^ (r & 7)) << 4));
         if ((*v & 0x7f80u) == 0x7f80u) {
             first = r;
             *v = 0;
         }
     }
-    smem[kBad + (c & (kRing - 1)) * 128 + p] = (unsigned char)first;
+    bad[p] = (unsigned char)first;
     fence_async_smem();
+}
+// Such outputs of a column from there on, in the tile that leaves.
+__device__ __noinline__ void spoil(unsigned char *tile, const unsigned char *any, const unsigned char *bad,
+                                   int lane) {
+    int from = any[0] ? bad[0] : kC;
+    if (from == kC && any[1]) from = bad[128];
+    for (int r = from; r < kC; ++r)
+        *reinterpret_cast<uint16_t *>(tile + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                                      (lane & 7) * 2) = 0x7fff;
 }
 
 template <int DK, int PASS>
@@ -280,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gdr_ssm_chunk_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SeqTable table,
                          const __grid_constant__ Maps maps, int *err) {
     constexpr bool OUT = PASS != 1;
+    constexpr int kChain = DK > 64 ? 8 : 4;  // warps
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -302,12 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
-            const int n = i == GFREE || i == WX || i == WX + 1 || i == YFREE || i == YFREE + 1 || i == YSCALED
-                              ? 128
-                          : i == MFULL || i == MFULL + 1                ? 256
-                          : i == DFREE || i == SFULL               ? 4 * DK
+            const int n = i >= WX && i < WX + 2 || i == GFREE || i == YFREE || i == YFREE + 1 || i == YSCALED ? 128
+                          : i == MFULL || i == MFULL + 1              ? 256 + 128
+                          : i == DFREE || i == SFULL                  ? 32 * kChain
                           : i < EMPTY || (i < EMPTY + kStages && OUT) ? 2
-                                                                     : 1;
+                                                                      : 1;
             mbar_init(&bars[i], n);
         }
         *abort_flag = 0;
@@ -327,6 +363,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *slot;
     const uint32_t bar0 = smem_u32(bars), abort0 = smem_u32(smem + kAbort);
     auto wait = [&](int id, uint32_t parity) { wait_bounded(bar0 + 8 * id, parity & 1, abort0); };
+    // Two or three at once, a lane each: a wait whose phase has long ended still
+    // takes some 180 cycles of this busy kernel.  (The phase before a barrier's
+    // first counts as ended.)
+    auto wait2 = [&](int i0, uint32_t p0, int i1, uint32_t p1) {
+        wait(lane & 1 ? i1 : i0, lane & 1 ? p1 : p0);
+        __syncwarp();
+    };
+    auto wait3 = [&](int i0, uint32_t p0, int i1, uint32_t p1, int i2, uint32_t p2) {
+        wait2(lane & 2 ? i2 : i0, lane & 2 ? p2 : p0, i1, p1);
+    };
     auto scal = [&](int c, uint32_t what) {
         return reinterpret_cast<float *>(smem + kScal + (c & (kRing - 1)) * kScalBytes + what);
     };
@@ -344,9 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Stage at;
 
-    if (warp < DK / 8) {
+    if (warp < kWx0)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsChain));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp < kChain) {
         // ================= chain
-        constexpr int NH = 32;
+        constexpr int NH = 4 * DK / kChain;
         const int p = 32 * (warp & 3) + lane, n0 = NH * (warp >> 2);
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const bool on = 32 * (warp & 3) < dv;  // dv is a multiple of 32
@@ -377,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
             if (OUT) {
-                if (c > 0) wait(SFREE, c - 1);
+                wait(SFREE, c - 1);
                 if (on) {
 #pragma unroll
                     for (int g = 0; g < NH / 16; ++g) {
@@ -396,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[SFULL]);
             }
             const float now = dec;
+            if (c + 1 < NC) wait(FULL + at.st, at.ph);
             if (c + 1 < NC) {
-                wait(FULL + at.st, at.ph);
                 dec = scal(c + 1, kEnd)[0];
                 ref = scal(c + 1, kEnd)[1];
             }
@@ -409,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int g = 0; g < NH / W; ++g) {
                     float d[W];
                     tmem_ld16(tl + kTmD + n0 + W * g, d);
+                    if (g == NH / W - 1) {  // dS is free before the last of it is added
+                        tc_fence_before_sync();
+                        mbar_arrive(&bars[DFREE]);
+                    }
 #pragma unroll
                     for (int m = 0; m < W; m += 2) {
                         const float2 q = fma2(make_float2(now, now),
@@ -419,8 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            tc_fence_before_sync();
-            mbar_arrive(&bars[DFREE]);
+            if (!on) mbar_arrive(&bars[DFREE]);
         }
         float *end = PASS == 1 ? a.seg_state + ((size_t)unit * a.HV + hv) * per
                      : a.ht && last ? a.ht + ((size_t)u.seq * a.HV + hv) * per
@@ -434,57 +487,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         // no columns for these
     } else if (warp < kOut0) {
         // ================= (w x)^T: value columns over the lanes, two tokens a column
-        const int p0 = 32 * (warp & 3);
-        const uint32_t tl = tmem + ((uint32_t)p0 << 16);
+        const int wq = warp & 3, half = (warp >> 2) & 1, p0 = 32 * wq, t0 = 32 * half;
+        const uint32_t tw = tmem + ((uint32_t)p0 << 16) + kTmW + 48 * half;
         const bool on = p0 < dv;
         // this lane's row of the 8 x 8 blocks (tokens 8 j + row, columns p0 + 8 i ..):
         // matrices 0 and 1 of a load are adjacent columns, 2 and 3 the next tokens
         const int row = lane & 7;
-        const uint32_t x0 = smem_u32(smem) + kX + (p0 >> 6) * 8192 + ((lane >> 4) * 8 + row) * 128;
+        const uint32_t x0 = smem_u32(smem) + kX + (p0 >> 6) * 8192 + (t0 + (lane >> 4) * 8 + row) * 128;
         const int unit = ((p0 & 63) >> 3) + ((lane >> 3) & 1);
         for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
-            const int st = at.st, L = rows_in(c);
-            wait(FULL + st, at.ph);
-            if (L < kC) wait(FIX, 0);
-            if (c >= 2) wait(WFREE + (c & 1), (c >> 1) - 1);
+            const int st = at.st;
+            if (OUT)  // the last for the arrival below
+                wait3(FULL + st, at.ph, WFREE + half, c - 1, MFREE + (c & 1), (c >> 1) - 1);
+            else
+                wait2(FULL + st, at.ph, WFREE + half, c - 1);
+            if (rows_in(c) < kC) wait(FIX, 0);
             tc_fence_after_sync();
+            bool any = false;
             if (on) {
-                const uint2 *w = reinterpret_cast<const uint2 *>(scal(c, kW)) + (lane & 3);
-                const uint32_t tw = tl + kTmW + 64 * (c & 1);
+                const uint4 *w = reinterpret_cast<const uint4 *>(scal(c, kW)) + 16 * half + (lane & 3);
                 uint32_t odd = 0;  // NaN where a value is not finite
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    const int hh = k & 1, s32 = k >> 1;  // half of the columns, of the tokens
-                    const uint32_t x = x0 + st * kStage + s32 * 4096 + (((unit + 2 * hh) ^ row) << 4);
-                    uint32_t q[8], h[8], l[8];
+                for (int hh = 0; hh < 2; ++hh) {  // half of the columns
+                    const uint32_t x = x0 + st * kStage + (((unit + 2 * hh) ^ row) << 4);
+                    uint32_t q[8], h[8], m[8], l[8];
                     ldsm4_t(x, *reinterpret_cast<uint32_t (*)[4]>(q));
                     ldsm4_t(x + 2048, *reinterpret_cast<uint32_t (*)[4]>(q + 4));
-                    if (OUT)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(q[j]), "r"(0));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint2 ww = w[16 * s32 + 4 * j];
-                        weigh2(q[2 * j], ww.x, ww.y, h[2 * j], l[2 * j]);
-                        weigh2(q[2 * j + 1], ww.x, ww.y, h[2 * j + 1], l[2 * j + 1]);
+                        const uint4 ww = w[4 * j];
+                        if (OUT)
+                            asm("fma.rn.bf16x2 %0, %1, %3, %0;\n\tfma.rn.bf16x2 %0, %2, %3, %0;"
+                                : "+r"(odd)
+                                : "r"(q[2 * j]), "r"(q[2 * j + 1]), "r"(0));
+                        weigh3(q[2 * j], ww, h[2 * j], m[2 * j], l[2 * j]);
+                        weigh3(q[2 * j + 1], ww, h[2 * j + 1], m[2 * j + 1], l[2 * j + 1]);
                     }
-                    const uint32_t to = tw + ((uint32_t)(16 * hh) << 16) + 16 * s32;
+                    const uint32_t to = tw + ((uint32_t)(16 * hh) << 16);
                     tmem_st_16x128(to, h);
+                    tmem_st_16x128(to + 16, m);
                     tmem_st_16x128(to + 32, l);
                 }
+                if (OUT) any = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
                 tmem_st_wait();
-                if (OUT) {
-                    const bool any = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
-                    if (any) mask_odd(smem, st, c, p0 + lane);
-                    if (lane == 0)
-                        *reinterpret_cast<uint32_t *>(smem + kBadAt + (c & (kRing - 1)) * 16 + (warp & 3) * 4) = any;
-                }
             }
             tc_fence_before_sync();
-            mbar_arrive(&bars[WX + (c & 1)]);
+            mbar_arrive(&bars[WX + half]);
             if (OUT) {
-                if (c >= 2) wait(MFREE + (c & 1), (c >> 1) - 1);
+                if (on) {
+                    unsigned char *bad = smem + kBad + (c & (kRing - 1)) * 256 + 128 * half;
+                    if (any) mask_odd(smem, st, t0, bad, p0 + lane);
+                    if (lane == 0) smem[kBadAt + (c & (kRing - 1)) * 8 + 2 * wq + half] = any;
+                }
                 mbar_arrive(&bars[MFULL + (c & 1)]);
             }
         }
@@ -614,12 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[YFREE + (c & 1)]);
                 if (on) {
                     unsigned char *sc = so + (c & 1) * 16384;
-                    if (*reinterpret_cast<const uint32_t *>(smem + kBadAt + (c & (kRing - 1)) * 16 + wq * 4)) {
+                    const unsigned char *any = smem + kBadAt + (c & (kRing - 1)) * 8 + 2 * wq;
+                    if (*reinterpret_cast<const uint16_t *>(any)) {
                         // from a value of x on that is not finite
                         __syncwarp();
-                        for (int r = smem[kBad + (c & (kRing - 1)) * 128 + 32 * wq + lane]; r < kC; ++r)
-                            *reinterpret_cast<uint16_t *>(sc + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
-                                                          (lane & 7) * 2) = 0x7fff;
+                        spoil(sc, any, smem + kBad + (c & (kRing - 1)) * 256 + 32 * wq + lane, lane);
                     }
                     if (L == kC) {
                         fence_async_smem();
@@ -655,10 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tl = tmem + ((uint32_t)(32 * sw) << 16);
             const float D = a.D ? a.D[hv] : 0.f;
             for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
-                wait(FULL + at.st, at.ph);
-                wait(GRAM, c);
+                wait3(FULL + at.st, at.ph, GRAM, c, MFREE + (c & 1), (c >> 1) - 1);
                 tc_fence_after_sync();
-                if (c >= 2) wait(MFREE + (c & 1), (c >> 1) - 1);
                 unsigned char *m = smem + kM + (c & 1) * 16384 + kmajor_off(t, 0, kC);
                 const bool far = scal(c, kEnd)[2] != 0.f;
                 const float diag = far ? D : scal(c, kDiag)[t], ct = far ? scal(c, kCum)[t] : 0.f;
@@ -801,9 +852,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p0 = before + c0, p1 = before + c1;
             // (a sum that is not a number counts as beyond: it would reach all of r's chunk)
             const bool far = __any_sync(0xffffffffu, !(fabsf(p0 - r) <= kRange && fabsf(p1 - r) <= kRange));
-            uint2 w;
-            pair2(fast_exp2(behind + f0) * s0, fast_exp2(behind + f1) * s1, w.x, w.y);
-            *reinterpret_cast<uint2 *>(q + kW / 4) = w;
+            float w0[3], w1[3];
+            split_weight(fast_exp2(behind + f0) * s0, w0[0], w0[1], w0[2]);
+            split_weight(fast_exp2(behind + f1) * s1, w1[0], w1[1], w1[2]);
+            *reinterpret_cast<uint4 *>(scal(c, kW) + 4 * lane) =
+                make_uint4(pack2(w0[0], w1[0]), pack2(w0[1], w1[1]), pack2(w0[2], w1[2]), 0);
             if (!far) {
                 const float v0 = fast_exp2(r - p0), v1 = fast_exp2(r - p1);
                 put(kE, fast_exp2(p0 - r), fast_exp2(p1 - r));
@@ -859,20 +912,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = at.st;
             const uint64_t o = (uint64_t)(st * (kStage >> 4));
             at.next();
-            wait(WX + (c & 1), c >> 1);
-            wait(DFREE, c);
-            tc_fence_after_sync();
-            if (elect_one()) {
-                // hi, then lo, against the same rows
-                products<true>(tmem + kTmD, tmem + kTmW + 64 * (c & 1), 8, 0, dBt + o, 128, -512, idD, 8, 0);
-                mma_commit(&bars[DELTA]);
-                mma_commit(&bars[WFREE + (c & 1)]);
-                mma_commit(&bars[EMPTY + st]);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // 32 tokens at a time: three numbers against the same rows
+                if (h == 0)
+                    wait2(DFREE, c, WX, c);
+                else
+                    wait(WX + 1, c);
+                tc_fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 6; ++k)
+                        mma_bf16_ts(tmem + kTmD, tmem + kTmW + 48 * h + 8 * k,
+                                    dBt + o + 256 * h + 128 * (k & 1), idD, h + k > 0);
+                    mma_commit(&bars[WFREE + h]);
+                    if (h) {
+                        mma_commit(&bars[DELTA]);
+                        mma_commit(&bars[EMPTY + st]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
             if (OUT && c + 1 < NC) {
-                wait(FULL + at.st, at.ph);
-                wait(GFREE, c);
+                wait2(FULL + at.st, at.ph, GFREE, c);
                 tc_fence_after_sync();
                 gram(at.st);
             }
@@ -892,9 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
             const uint64_t o = (uint64_t)(at.st * (kStage >> 4)), m = dM + (uint64_t)((c & 1) * 1024);
             const uint32_t y = tmem + kTmY + 64 * (c & 1);
-            wait(FULL + at.st, at.ph);
-            wait(SFULL, c);
-            if (c >= 2) wait(YFREE + (c & 1), (c >> 1) - 1);
+            wait3(FULL + at.st, at.ph, SFULL, c, YFREE + (c & 1), (c >> 1) - 1);
             const bool far = scal(c, kEnd)[2] != 0.f;
             tc_fence_after_sync();
             if (elect_one()) {
