@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads)
 // Sequences of one token (or none): one CTA per (sequence, value head) passes
 // its state through registers once, 16 bytes a thread and row; a warp's row
 // or rows are adjacent, and all of a thread's loads are in flight together.
+// 64 sequences of 32 heads of 128 x 128: 42 us, 6.4 TB/s (the walk takes 86).
 constexpr int kStepWarps = 8;
 
 template <typename T, int DK, int DV>
@@ -329,7 +330,10 @@ int sm_count() {
 // so walks are cut where that is estimated to be faster.  Costs are in rows of
 // a full walk; a walk to the end state alone, the second launch and the start
 // from the segments before were measured (chunks: one CTA an SM; walk: kWalkCtas
-// of them, a token's latency being the same up to there).
+// of them, a token's latency being the same up to there).  One sequence of 32
+// gated heads of 128 x 128, us a call whole / cut: 1024 tokens 50 / 40 (by three),
+// 4096 174 / 83 (by four, the best of up to twelve), 16384 663 / 257 (by four;
+// 254 by nine); two of 4096 174 / 136 (by two, the best).
 int choose_segment(const int *cu, int N, int T, int HV, int dv, int longest, bool chunks) {
     constexpr int kWalkCtas = 4;
     const int sms = sm_count(), grain = chunks ? 64 : 16;
@@ -380,16 +384,16 @@ Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, int dtype, u
 
 // Whether bf16 sequences are so short that walking them token by token is
 // faster than chunks, by what both cost (microseconds): a CTA of the chunk
-// kernel 8 for itself and 1.4 a chunk, one an SM; the walk its operations at 20
+// kernel 9 for itself and 1.5 a chunk, one an SM; the walk its operations at 20
 // TFLOP/s and its states at memory's rate.  64 sequences of 32 heads of 128 x
-// 128: chunks 128 (2 to 16 tokens), walk 97 (2), 110 (4), 137 (8), 173 (16); of
-// 64 x 64, 16 tokens: chunks 90, walk 37.
+// 128: chunks 146 (2 to 16 tokens), walk 97 (2), 110 (4), 136 (8), 173 (16); of
+// 64 x 64, 16 tokens: chunks 90, walk 38.
 bool walk_is_faster(const SsmArgs &a, const Plan &plan) {
     const int sms = sm_count();
     if (sms == 0) return false;
     const double rows = a.cu ? a.cu[a.N] : (double)a.N * a.T, state = (double)a.dk * a.dv;
     const double waves = (double)((plan.units * a.HV + sms - 1) / sms);
-    const double chunks = waves * (8.0 + 1.4 * (rows / 64 / plan.units < 1 ? 1 : rows / 64 / plan.units));
+    const double chunks = waves * (9.0 + 1.5 * (rows / 64 / plan.units < 1 ? 1 : rows / 64 / plan.units));
     const double walk = rows * a.HV * 5 * state / 20e6 + a.N * a.HV * state * 8 / 6e6 + 0.2 * plan.longest;
     return walk < chunks;
 }
