@@ -542,8 +542,8 @@ GDR_API gdr_status gdr_state_load(const signed char *cache, const float *scale, 
  *
  * A sum is formed in float32 and rounded once.  Supported: D >= 1, W in
  * {2, 3, 4}, ldx, ldo >= D, D below 2^23; x, out, s0 and st aligned to their
- * elements, w and bias 4-byte.  Fast (16 bytes at a time) where those four are
- * 16-byte aligned and D, ldx and ldo multiples of 16 bytes.  flags:
+ * elements, w and bias 4-byte.  Fast (four channels at a time) where those four
+ * are aligned to four elements and D, ldx and ldo multiples of four.  flags:
  * GDR_FLAG_SILU or 0.
  */
 #define GDR_FLAG_SILU 0x40000u
@@ -608,7 +608,7 @@ GDR_API gdr_status gdr_qk_norm(const void *q, const void *k, const float *weight
  * rounded; bf16 sequences run by chunks of 64 tokens on the tensor cores (x, b
  * and c 16-byte aligned, their distances multiples of 16 bytes; otherwise token by
  * token, as f32 and short ones), where the outputs read a copy of the state
- * rounded to bf16.  A value that is not finite reaches no output of an earlier
+ * rounded to bf16 and what a token adds to the state is off by 8e-7 of it (rms).  A value that is not finite reaches no output of an earlier
  * token; from there on its column (x, z) or head comes out as NaN or infinite.
  *
  * `workspace`: device memory of gdr_ssm_workspace_bytes(...) bytes, 256-byte
