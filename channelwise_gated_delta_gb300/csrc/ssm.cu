@@ -8,8 +8,11 @@
 // columns); warp w holds the rows w dk / 4 .. of the columns of its lanes in
 // registers, so that a token is three operations an element of the state (two
 // elements at a time) and no exchange: the four warps' partial outputs meet in
-// shared memory once every kTok tokens.  It is bound by those operations and
-// the loads of b and c from shared memory that feed them.
+// shared memory once every kTok tokens, and the next ones' inputs (z too: read
+// where it is used it cost 565 us in place of 394) are on their way meanwhile.
+// 4 x 1024 tokens of 32 gated heads of 128 x 128, f32: 394 us, where the operations
+// at two a lane and cycle take 172 on all SMs and 205 as its 256 CTAs lie; the
+// rest is latency, of the loads of b and c from shared memory before all.
 // gdr_ssm_step_kernel is one pass over the states of single tokens, bound by
 // memory; bf16 sequences take the chunks of ssm_tc.cu.
 #include <limits.h>
@@ -72,12 +75,13 @@ __global__ void __launch_bounds__(kThreads)
     const T *x = static_cast<const T *>(a.x) + u.row0 * a.ldx + (size_t)hv * a.dv + tile * kCols;
     const T *b = static_cast<const T *>(a.b) + u.row0 * a.ldb + (size_t)hk * DK;
     const T *c = static_cast<const T *>(a.c) + u.row0 * a.ldc + (size_t)hk * DK;
+    const T *z = a.z ? static_cast<const T *>(a.z) + u.row0 * a.ldz + (size_t)hv * a.dv + tile * kCols : nullptr;
     const float *dt = a.dt + u.row0 * a.HV + hv;
     const float A = a.A[hv], bias = a.dt_bias ? a.dt_bias[hv] : 0.f, D = a.D ? a.D[hv] : 0.f;
     float total = 0.f;
 
     constexpr int NB = kTok * DK / kThreads, NX = kTok * kCols / kThreads;
-    float rb[NB], rc[NB], rx[NX], rdt = 0.f;
+    float rb[NB], rc[NB], rx[NX], rz[NX], gate[NX], rdt = 0.f;
     auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -90,6 +94,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < NX; ++i) {
             const int e = tid + kThreads * i, k = e / kCols;
             rx[i] = t + k < t1 ? to_f32(x[(t + k) * a.ldx + e % kCols]) : 0.f;
+            if (PASS != 1) rz[i] = a.z && t + k < t1 ? to_f32(z[(t + k) * a.ldz + e % kCols]) : 0.f;
         }
         if (tid < kTok && t + tid < t1) rdt = dt[(long long)(t + tid) * a.HV];
     };
@@ -105,6 +110,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < NX; ++i) {
             const int e = tid + kThreads * i;
             sx[e / kCols][e % kCols] = rx[i];
+            if (PASS != 1) gate[i] = rz[i];
         }
         if (tid < kTok) {
             const float step = t + tid < t1 ? ssm_step(rdt, bias, a.softplus) : 0.f;
@@ -115,17 +121,17 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads();
         if (t + kTok < t1) fetch(t + kTok);
         const int n = min(kTok, t1 - t);
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float keep = sdec[k];
             if (PASS == 1) total += slog[k];
             const float2 keep2 = make_float2(keep, keep);
-            float2 xs[COLS], y[COLS], z[COLS];
+            float2 xs[COLS], y[COLS], y2[COLS];
 #pragma unroll
             for (int j = 0; j < COLS; ++j) {
                 const float q = sstep[k] * sx[k][lane + 32 * j];
                 xs[j] = make_float2(q, q);
-                y[j] = z[j] = make_float2(0.f, 0.f);
+                y[j] = y2[j] = make_float2(0.f, 0.f);
             }
 #pragma unroll
             for (int r = 0; r < R; r += 4) {
@@ -139,13 +145,13 @@ __global__ void __launch_bounds__(kThreads)
                     s1 = fma2(keep2, s1, mul2(make_float2(bv.z, bv.w), xs[j]));
                     if (PASS != 1) {
                         y[j] = fma2(make_float2(cv.x, cv.y), s0, y[j]);
-                        z[j] = fma2(make_float2(cv.z, cv.w), s1, z[j]);
+                        y2[j] = fma2(make_float2(cv.z, cv.w), s1, y2[j]);
                     }
                 }
             }
             if (PASS != 1)
 #pragma unroll
-                for (int j = 0; j < COLS; ++j) part[warp][k][lane + 32 * j] = (y[j].x + y[j].y) + (z[j].x + z[j].y);
+                for (int j = 0; j < COLS; ++j) part[warp][k][lane + 32 * j] = (y[j].x + y[j].y) + (y2[j].x + y2[j].y);
         }
         __syncthreads();
         if (PASS != 1) {
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(kThreads)
                 y = fmaf(D, sx[k][col], y);
                 const size_t row = (size_t)(u.row0 + t + k);
                 const size_t o = (size_t)hv * a.dv + tile * kCols + col;
-                if (a.z) y = ssm_gate(y, to_f32(static_cast<const T *>(a.z)[row * a.ldz + o]));
+                if (a.z) y = ssm_gate(y, gate[i]);
                 static_cast<T *>(a.out)[row * a.HV * a.dv + o] = from_f32<T>(y);
             }
             __syncthreads();
@@ -288,7 +294,7 @@ cudaError_t launch_cols(const SsmArgs &a, cudaStream_t stream) {
     });
 }
 // Two columns a lane read each row of b and c half as often: f32, 4 x 1024
-// tokens of 32 heads of 128 x 128, 377 us against 458.  Below a CTA for each of
+// tokens of 32 gated heads of 128 x 128, 394 us against 485.  Below a CTA for each of
 // kWideSms SMs the narrow ones are twice as many and no slower each.
 template <typename T, int DK, int PASS>
 cudaError_t launch_walk(const SsmArgs &a, cudaStream_t stream) {
@@ -329,28 +335,32 @@ int sm_count() {
 // Rows of a segment: few heads leave SMs idle while a long sequence is walked,
 // so walks are cut where that is estimated to be faster.  Costs are in rows of
 // a full walk; a walk to the end state alone, the second launch and the start
-// from the segments before were measured (chunks: one CTA an SM; walk: kWalkCtas
-// of them, a token's latency being the same up to there).  One sequence of 32
-// gated heads of 128 x 128, us a call whole / cut: 1024 tokens 50 / 40 (by three),
-// 4096 174 / 83 (by four, the best of up to twelve), 16384 663 / 257 (by four;
-// 254 by nine); two of 4096 174 / 136 (by two, the best).
-int choose_segment(const int *cu, int N, int T, int HV, int dv, int longest, bool chunks) {
-    constexpr int kWalkCtas = 4;
-    const int sms = sm_count(), grain = chunks ? 64 : 16;
+// from the segments before were measured.  An SM takes `full` CTAs of 32 columns
+// before they slow one another down: of the chunk kernel one, of the walk as many
+// as have 256 rows of states.  One sequence of 32 gated heads of 128 x 128, bf16, us a
+// call whole / cut: 1024 tokens 50 / 40 (by three), 4096 174 / 83 (by four, the
+// best of up to twelve), 16384 663 / 257 (by four; 254 by nine); two of 4096 174 / 136
+// (by two, the best).  f32, us on the device: 4096 tokens 670 / 537 (by eight; 520 by
+// 24); two of 2048 485 / 490 (by eight), not cut; 9 heads of 64 x 32, 4096
+// tokens 502 / 45.
+int choose_segment(const int *cu, int N, int T, int HV, int dk, int dv, int longest, bool chunks) {
+    const int sms = sm_count(), grain = chunks ? 64 : 16, full = chunks ? 1 : 256 / dk;
     const long long per = (long long)HV * (chunks ? 1 : dv / 32);
-    const long long slots = (long long)sms * (chunks ? 1 : kWalkCtas);
-    if (sms == 0 || longest < 4 * grain || N * per >= slots) return INT_MAX;
+    if (sms == 0 || longest < 4 * grain || N * per >= (long long)sms * full) return INT_MAX;
     const double state_only = 0.5, launch = chunks ? 256 : 32, start = chunks ? 24 : 4;
-    double best = longest;
+    auto slower = [&](long long ctas) {
+        const double on_an_sm = (double)((ctas + sms - 1) / sms);
+        return on_an_sm > full ? on_an_sm / full : 1.0;
+    };
+    double best = 0.9 * longest;  // cut for a tenth at least
     int rows = INT_MAX;
     for (int cut = 2; cut <= 64; ++cut) {
         const int r = ((longest + cut - 1) / cut + grain - 1) / grain * grain;
         if (r >= longest) continue;
         const long long units = count_units(cu, N, T, r), after = units - N;
-        const double cost = (double)((units * per + slots - 1) / slots) * r +
-                            state_only * (double)((after * per + slots - 1) / slots) * r + launch +
+        const double cost = (slower(units * per) + state_only * slower(after * per)) * r + launch +
                             start * (longest / r);
-        if (cost < 0.9 * best) {
+        if (cost < best) {
             best = cost;
             rows = r;
         }
@@ -368,7 +378,7 @@ Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, int dtype, u
             const int rows = ((longest + forced - 1) / forced + 63) / 64 * 64;
             if (rows < longest) p.seg_rows = rows;
         } else if (forced == 0) {
-            p.seg_rows = choose_segment(cu, N, T, HV, dv, longest,
+            p.seg_rows = choose_segment(cu, N, T, HV, dk, dv, longest,
                                         dtype == GDR_BF16 && !(flags & GDR_FLAG_FORCE_GENERIC));
         }
     }
@@ -386,8 +396,8 @@ Plan make_plan(const int *cu, int N, int T, int HV, int dk, int dv, int dtype, u
 // faster than chunks, by what both cost (microseconds): a CTA of the chunk
 // kernel 9 for itself and 1.5 a chunk, one an SM; the walk its operations at 20
 // TFLOP/s and its states at memory's rate.  64 sequences of 32 heads of 128 x
-// 128: chunks 146 (2 to 16 tokens), walk 97 (2), 110 (4), 136 (8), 173 (16); of
-// 64 x 64, 16 tokens: chunks 90, walk 38.
+// 128: chunks 146 (2 to 16 tokens), walk 97 (2), 113 (4), 142 (8), 174 (16); of
+// 64 x 64, 16 tokens: chunks 90, walk 40.
 bool walk_is_faster(const SsmArgs &a, const Plan &plan) {
     const int sms = sm_count();
     if (sms == 0) return false;
