@@ -22,8 +22,8 @@
 //     dS = (w x)^T b        (w x)^T in tensor memory, b as it came
 // x, b and c are exact.  w x goes in as three bf16 numbers (see weigh3), off by
 // 8e-7 of it: the state, which is float32 in registers and never rounded itself,
-// keeps float32's accuracy but for that.  (A pair is off by 4e-6, and 406 us
-// where three take 405: the products are not what the kernel waits for.)  M goes
+// keeps float32's accuracy but for that.  (A pair is off by 4e-6, and took 406 us
+// where three take 400: the products are not what the kernel waits for.)  M goes
 // in as a pair hi + lo, off by 2^-16.  The copy of S that Y reads is rounded
 // once to bf16: its error is averaged over dk products and adds 1 to 27 % to
 // what the output's own rounding leaves (M rounded the same way would add 26
@@ -46,7 +46,7 @@
 //            ahead), and a thread that waits for one product's inputs feeds no other
 // The chain's registers (112 a thread) come from the others (56).
 //
-// What bounds it: 4 x 16384 tokens of 32 heads of 128 take 405 us, 3000 cycles a
+// What bounds it: 4 x 16384 tokens of 32 heads of 128 take 400 us, 3000 cycles a
 // chunk.  Its products take 1790 of them, its bytes 1820 (at 6.8 TB/s).
 // The rest is one chunk's way around: products of dS 770, its read 200, S 600 to
 // 900, the next products' start 200, with the other products in between.  With
