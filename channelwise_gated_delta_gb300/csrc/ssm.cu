@@ -353,10 +353,11 @@ int choose_segment(const int *cu, int N, int T, int HV, int dk, int dv, int long
         return on_an_sm > full ? on_an_sm / full : 1.0;
     };
     double best = 0.9 * longest;  // cut for a tenth at least
-    int rows = INT_MAX;
-    for (int cut = 2; cut <= 64; ++cut) {
-        const int r = ((longest + cut - 1) / cut + grain - 1) / grain * grain;
-        if (r >= longest) continue;
+    int rows = INT_MAX, r = longest;
+    for (int cut = 2; cut <= 64 && r > grain; ++cut) {
+        const int last = r;
+        r = ((longest + cut - 1) / cut + grain - 1) / grain * grain;
+        if (r >= longest || r == last) continue;
         const long long units = count_units(cu, N, T, r), after = units - N;
         const double cost = (slower(units * per) + state_only * slower(after * per)) * r + launch +
                             start * (longest / r);
