@@ -90,8 +90,8 @@ constexpr uint32_t kX = 0, kB = kTile, kCm = 2 * kTile, kStage = 3 * kTile;
 constexpr uint32_t kM = kStages * kStage;           // [2] x {hi, lo} [64 t][64 s]
 constexpr uint32_t kScal = kM + 2 * 16384;          // [kRing] of the following
 // of a chunk, 64 numbers each: exp(cum - r), exp(r - cum) step, D exp(r - cum);
-// in a chunk beyond r's range kV the sums behind and kCum up to a token within
-// its half, and the steps; of every two tokens w's three parts and a gap; then
+// in a chunk beyond r's range kCum the sums up to a token from its 16 tokens'
+// first, and the steps; of every two tokens w's three parts and a gap; then
 // exp(cum_end), exp(r) and whether the chunk is beyond r's range
 constexpr uint32_t kE = 0, kV = 256, kDiag = 512, kCum = 768, kStep = 1024, kW = 1280, kEnd = 1792;
 constexpr uint32_t kScalBytes = 1808;
@@ -706,13 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // behind the sequence's end makes outputs that go nowhere.)
             const int g0 = (warp - kScore0) >> 2;
             const uint32_t tl = tmem + ((uint32_t)(32 * sw) << 16);
-            const float D = a.D ? a.D[hv] : 0.f;
+            const float D = a.D ? a.D[hv] : 0.f, A2 = a.A[hv] * kLog2e;
             for (int c = 0; c < NC && !*abort_flag; ++c, at.next()) {
                 wait3(FULL + at.st, at.ph, GRAM, c, MFREE + (c & 1), (c >> 1) - 1);
                 tc_fence_after_sync();
                 unsigned char *m = smem + kM + (c & 1) * 16384 + kmajor_off(t, 0, kC);
                 const bool far = scal(c, kEnd)[2] != 0.f;
-                const float diag = far ? D : scal(c, kDiag)[t], ct = far ? scal(c, kCum)[t] : 0.f;
+                const float diag = far ? D : scal(c, kDiag)[t];
 #pragma unroll 1
                 for (int g = g0; g < 2 * sw + 2; g += 2) {
                     float d[16], w[16];
@@ -722,13 +722,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4 *>(w + e) =
                                 *reinterpret_cast<const float4 *>(scal(c, kV) + 16 * g + e);
                     } else {
-                        // exp(cum_t - cum_s) step_s from sums within the halves:
-                        // up to t less up to s, or, across them, plus those behind s
-                        const bool across = 16 * g < 32 * sw;
-                        const float *q = scal(c, across ? kV : kCum) + 16 * g, sign = across ? 1.f : -1.f;
+                        // exp(cum_t - cum_s) step_s, its exponent the sum of the tokens behind
+                        // s up to t, from t's end on: what stands behind these 16 tokens,
+                        // then one more of them a column.  (A difference of two sums would
+                        // lose the slow decays beside a token that is large: 2^-24 of the sums.)
+                        const float *step = scal(c, kStep) + 16 * g, *up = scal(c, kCum);
+                        const int mine = t - 16 * g, quarter = t >> 4;
+                        float sum = quarter > g ? up[t] : 0.f;
+                        if (g < 1 && quarter > 1) sum += up[31];
+                        if (g < 2 && quarter > 2) sum += up[47];
+                        w[15] = fast_exp2(sum) * step[15];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[e] = fast_exp2(fmaf(sign, q[e], ct)) * scal(c, kStep)[16 * g + e];
+                        for (int e = 14; e >= 0; --e) {
+                            if (e < mine) sum = fmaf(step[e + 1], A2, sum);
+                            w[e] = fast_exp2(sum) * step[e];
+                        }
                     }
                     tmem_ld16(tl + kTmG + 16 * g, d);
                     if (g >= 2 * sw) {  // the warp's last: G is free again
@@ -866,9 +874,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // kE rescales the part from the state; M is as it is, without D:
                 // its columns of ones are what the outputs are scaled by
                 r = 0.f;
+                float in = l0 + l1;
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) {
+                    const float o = __shfl_up_sync(0xffffffffu, in, off, 8);
+                    if ((lane & 7) >= off) in += o;
+                }
+                in = __shfl_up_sync(0xffffffffu, in, 1, 8);
+                in = ((lane & 7) ? in : 0.f) + l0;
                 put(kE, fast_exp2(p0), fast_exp2(p1));
-                put(kV, f0, f1);
-                put(kCum, c0, c1);
+                put(kCum, in, in + l1);
                 put(kStep, s0, s1);
                 put(kDiag, 1.f, 1.f);
             }
