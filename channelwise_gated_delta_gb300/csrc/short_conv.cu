@@ -82,9 +82,10 @@ __global__ void __launch_bounds__(kThreads)
     const int c = (blockIdx.y * kThreads + threadIdx.x) * VEC;
     if (c >= D) return;
     const SeqUnit u = find_unit(table, blockIdx.x);
-    const int r0 = u.unit * rows, r1 = min(u.len, r0 + rows);
-    x += u.row0 * ldx + c;
-    out += u.row0 * ldo + c;
+    // rows count from the unit's first: a sequence may end where an int does
+    const int r0 = u.unit * rows, n = min(u.len - r0, rows);
+    x += (u.row0 + r0) * ldx + c;
+    out += (u.row0 + r0) * ldo + c;
     const size_t state = (size_t)u.seq * (W - 1) * D + c;
     auto row = [&](int t) { return __ldg(reinterpret_cast<const Raw *>(x + t * ldx)); };
 
@@ -93,12 +94,10 @@ __global__ void __launch_bounds__(kThreads)
     Raw before[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        const int t = r0 - (W - 1) + j;
-        if (t >= 0)
-            before[j] = row(t);
+        if (r0 > 0)
+            before[j] = row(j - (W - 1));
         else
-            before[j] = s0 ? *reinterpret_cast<const Raw *>(s0 + state + (size_t)(W - 1 + t) * D)
-                           : V::zero();
+            before[j] = s0 ? *reinterpret_cast<const Raw *>(s0 + state + (size_t)j * D) : V::zero();
     }
     float win[W - 1][VEC], tap[W][VEC], b[VEC];
 #pragma unroll
@@ -134,13 +133,13 @@ __global__ void __launch_bounds__(kThreads)
     // kStep rows at a time, the next ones on their way meanwhile
     Raw in[kStep];
 #pragma unroll
-    for (int k = 0; k < kStep; ++k) in[k] = r0 + k < r1 ? row(r0 + k) : V::zero();
-    for (int t0 = r0; t0 < r1; t0 += kStep) {
+    for (int k = 0; k < kStep; ++k) in[k] = k < n ? row(k) : V::zero();
+    for (int t0 = 0; t0 < n; t0 += kStep) {
         Raw next[kStep];
-        const bool whole = t0 + 2 * kStep <= r1;
+        const bool whole = t0 + 2 * kStep <= n;
 #pragma unroll
         for (int k = 0; k < kStep; ++k)
-            next[k] = whole || t0 + kStep + k < r1 ? row(t0 + kStep + k) : V::zero();
+            next[k] = whole || t0 + kStep + k < n ? row(t0 + kStep + k) : V::zero();
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
             float f[VEC], y[VEC];
@@ -172,7 +171,7 @@ __global__ void __launch_bounds__(kThreads)
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
                 win[W - 2][v] = f[v];
             }
-            if (t0 + k < r1) *reinterpret_cast<Raw *>(out + (t0 + k) * ldo) = V::pack(y);
+            if (t0 + k < n) *reinterpret_cast<Raw *>(out + (t0 + k) * ldo) = V::pack(y);
         }
 #pragma unroll
         for (int k = 0; k < kStep; ++k) in[k] = next[k];
