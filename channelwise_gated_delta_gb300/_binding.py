@@ -271,6 +271,15 @@ def gdr_set_workspace(workspace, device=None):
     _registered_ws[workspace.device.index] = workspace
 
 
+_MOST_INT = 2 ** 31 - 1
+
+
+def _ints(*sizes):
+    """Refuses sizes that the library's ints would wrap (ctypes keeps the low 32 bits)."""
+    if max(sizes) > _MOST_INT:
+        raise ValueError("sizes of 2^31 and more are not supported, got %d" % max(sizes))
+
+
 def _cu_array(cu_seqlens):
     """cu_seqlens (a sequence of ints or a CPU integer tensor) as a ctypes int32 array."""
     if isinstance(cu_seqlens, torch.Tensor):
@@ -280,6 +289,7 @@ def _cu_array(cu_seqlens):
     vals = [int(x) for x in cu_seqlens]
     if not vals:
         raise ValueError("cu_seqlens needs at least one entry")
+    _ints(max(vals), -min(vals))
     return (ctypes.c_int * len(vals))(*vals), len(vals) - 1
 
 
@@ -656,6 +666,7 @@ def gdr_short_conv(x, weight, bias=None, cu_seqlens=None, s0=None, out=None, st=
         cu, n, T = None, shape[0], shape[1]
     else:
         cu, n, T = _sequences(shape, lead, cu_seqlens)
+    _ints(n, T, D)
     w_ptr = _checked("weight", weight, (D, W), torch.float32, index)
     bias_ptr = s0_ptr = st_ptr = None
     if bias is not None:
@@ -719,6 +730,7 @@ def gdr_qk_norm(q, k, weight_q=None, weight_k=None, positions=None, freqs=None, 
     rows = shape[0] if lead == 1 else shape[0] * shape[1]
     if kshape[:lead] != shape[:lead] or kshape[lead + 1] != d:
         raise ValueError("k must match q in rows and d")
+    _ints(HQ, HK, d)
     wq, wk = HQ * d, HK * d
     ldq = _rows_of("q", q, shape, lead, wq, dtype, index)
     ldk = _rows_of("k", k, kshape, lead, wk, dtype, index)
@@ -804,6 +816,7 @@ def gdr_ssm_forward(x, b, c, dt, a, d=None, z=None, dt_bias=None, cu_seqlens=Non
         cu, n, T = None, shape[0], shape[1]
     else:
         cu, n, T = _sequences(shape, lead, cu_seqlens)
+    _ints(n, T, HV, dv, HK, dk)
     if h0 is not None:
         h0_ptr = _checked("h0", h0, (n, HV, dk, dv), f32, index)
     if ht is not None:
