@@ -610,6 +610,11 @@ GDR_API gdr_status gdr_qk_norm(const void *q, const void *k, const float *weight
  * token, as f32 and short ones), where the outputs read a copy of the state
  * rounded to bf16 and what a token adds to the state is off by 8e-7 of it (rms).  A value that is not finite reaches no output of an earlier
  * token; from there on its column (x, z) or head comes out as NaN or infinite.
+ * A chunk's outputs are formed about the middle of its decay: where a head decays to 2^-n over a
+ * chunk, n <= 160, the sum over its tokens of |x| (|c . b| step + |D|) has to stay below 2^(127 - n/2)
+ * (an output beyond that is infinite or NaN, never another number), and elements of the state below
+ * 2^(n/2 - 126) may count as zeros in its outputs.  At n = 160 (1.7 nats a token) these are
+ * 2^47 and 2^-46.  Faster decays, the state itself and sequences token by token have float32's range.
  *
  * `workspace`: device memory of gdr_ssm_workspace_bytes(...) bytes, 256-byte
  * aligned, untouched by anything else until the stream has passed the call;
