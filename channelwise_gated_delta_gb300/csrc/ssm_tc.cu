@@ -55,8 +55,10 @@
 // The rest is one chunk's way around: products of dS 770, its read 200, S 600 to
 // 900, the next products' start 200, with the other products in between.  With
 // all arithmetic of the warps taken out it takes 380.
-// Every wait is bounded: a timeout sets the CTA's abort flag and the library's
-// error word, and everyone runs out its loop.
+// Every wait is bounded (one second, of which a role may make three before it
+// looks): a timeout sets the CTA's abort flag and the library's error word, and
+// everyone runs out its loop.  Few instructions a wait: the warps run eight
+// different programs out of one instruction cache.
 #include <cuda.h>
 #include <limits.h>
 
@@ -83,8 +85,6 @@ constexpr int kRegsLaunch = 72, kRegsChain = 112, kRegsOther = 56;
 static_assert(2 * kRegsChain + 5 * kRegsOther == 7 * kRegsLaunch && kThreads * kRegsLaunch <= 65536, "registers");
 constexpr int kStages = 3;
 constexpr int kRing = 8;  // chunks whose scalars are held
-// a wait's limit: tries, of some 50 cycles each at least
-constexpr int kTries = 1 << 25;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -160,26 +160,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&h);
 }
-// Waits for a phase of the barrier; where it has not come in kTries tries (a
-// second or more), sets the CTA's abort flag and goes on: every warp looks at
-// the flag once a chunk.  As few instructions as that takes: the kernel's warps
-// run eight different programs out of one instruction cache.
-__device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b32 n;\n\t"
-        "mov.b32 n, %3;\n"
-        "TRY_%=:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
-        "@p bra DONE_%=;\n\t"
-        "add.s32 n, n, -1;\n\t"
-        "setp.ne.s32 p, n, 0;\n\t"
-        "@p bra TRY_%=;\n\t"
-        "st.volatile.shared.b32 [%2], 1;\n"
-        "DONE_%=:\n\t}" ::"r"(bar),
-        "r"(parity), "r"(abort_flag), "n"(kTries)
-        : "memory");
-}
-
 // (a, b) as hi + lo, two bf16 numbers each
 __device__ __forceinline__ void pair2(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack2(a, b);
@@ -366,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = *slot;
     const uint32_t bar0 = smem_u32(bars), abort0 = smem_u32(smem + kAbort);
-    auto wait = [&](int id, uint32_t parity) { wait_bounded(bar0 + 8 * id, parity & 1, abort0); };
+    // one second at most; every warp looks at the abort flag once a chunk
+    auto wait = [&](int id, uint32_t parity) { mbar_wait_cycles(bar0 + 8 * id, parity & 1, abort0); };
     // Two or three at once, a lane each: a wait whose phase has long ended still
     // takes some 180 cycles of this busy kernel.  (The phase before a barrier's
     // first counts as ended.)
@@ -698,8 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) {
                 bulk_wait_all();
-                if (*abort_flag && armed >= 0)  // a copy in flight lands before the CTA leaves
-                    mbar_wait_bounded(&bars[ZFULL + 4 * (armed & 1) + wq], (armed >> 1) & 1, kWaitNs);
+                if (*abort_flag)  // copies in flight land before the CTA leaves
+#pragma unroll 1
+                    for (int c = armed < 2 ? 0 : armed - 1; c <= armed; ++c)
+                        mbar_wait_bounded(&bars[ZFULL + 4 * (c & 1) + wq], (c >> 1) & 1, kWaitNs);
             }
         }
     } else if (warp != kScalars && warp != kIssueState && warp != kIssueY && warp != kLoads) {

@@ -26,8 +26,35 @@ __global__ void __launch_bounds__(32, 1)
     if (!mbar_wait_bounded(&bar, 0, limit_ns)) atomicAdd(gave_up, 1);
 }
 
+// The wait by cycles of the kernels with many short waits, 2^24 of them, by all 32
+// lanes; gave_up counts those that find the flag set.  ns: how long it took.
+__global__ void __launch_bounds__(32, 1)
+    gdr_selftest_cycles_kernel(int *gave_up, unsigned long long *ns) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int flag;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+        flag = 0;
+    }
+    __syncthreads();
+    const uint64_t t0 = global_timer_ns();
+    mbar_wait_cycles<1u << 24>(smem_u32(&bar), 0, smem_u32(&flag));
+    const uint64_t t1 = global_timer_ns();
+    if (*(volatile int *)&flag) atomicAdd(gave_up, 1);
+    if (threadIdx.x == 0) *ns = t1 - t0;
+}
+
 }  // namespace
 }  // namespace gdr
+
+// Launches the wait by cycles.
+extern "C" __attribute__((visibility("default"))) int gdr_diag_wait_cycles(
+    int *gave_up, unsigned long long *ns, void *stream) {
+    if (!gave_up || !ns) return -1;
+    gdr::gdr_selftest_cycles_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(gave_up, ns);
+    return (int)cudaGetLastError();
+}
 
 // Launches the wait on `stream` with a limit of limit_ns nanoseconds
 // (1 ms .. 1 s); `gave_up` a device int the kernel adds one to per thread

@@ -26,6 +26,8 @@ def _load():
         _lib.gdr_diag_umma.restype = i
         _lib.gdr_diag_wait_limit.argtypes = [ctypes.c_ulonglong, vp, vp]
         _lib.gdr_diag_wait_limit.restype = i
+        _lib.gdr_diag_wait_cycles.argtypes = [vp, vp, vp]
+        _lib.gdr_diag_wait_cycles.restype = i
     return _lib
 
 
@@ -63,3 +65,17 @@ def wait_limit(limit_ns, device="cuda"):
         raise RuntimeError("gdr_diag_wait_limit failed: %d" % st)
     torch.cuda.synchronize(device)
     return int(gave_up.item()), e0.elapsed_time(e1)
+
+
+def wait_cycles(device="cuda"):
+    """Runs the wait by cycles, 2^24 of them, on a barrier nothing arrives on (32 threads); returns
+    (threads that gave up, seconds that it took)."""
+    lib = _load()
+    gave_up = torch.zeros(1, dtype=torch.int32, device=device)
+    ns = torch.zeros(1, dtype=torch.int64, device=device)
+    st = lib.gdr_diag_wait_cycles(ctypes.c_void_p(gave_up.data_ptr()), ctypes.c_void_p(ns.data_ptr()),
+                                  ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+    if st != 0:
+        raise RuntimeError("gdr_diag_wait_cycles failed: %d" % st)
+    torch.cuda.synchronize(device)
+    return int(gave_up.item()), int(ns.item()) * 1e-9
