@@ -60,3 +60,20 @@ def test_drops_in_every_place_of_a_chunk():
         scale = want.float().abs().amax(0)
         assert ((out[rest, p] - want[:, 0]).float().abs() <= 2.0 ** -7 * scale).all(), p
         assert (ht[0, p] - end[0, 0]).abs().max() <= 2.0 ** -15 * end.abs().max(), p
+
+
+@pytest.mark.parametrize("flags", [0, gdr_flag_segments(2)])
+def test_steps_of_both_signs(flags):
+    """Without softplus a step may be negative: a token that grows the state and takes from it."""
+    d = dropping(3.0, 128, 64, 0.5, seed=3)
+    gen = torch.Generator().manual_seed(4)
+    d["dt"] *= torch.where(torch.rand(T, HV, generator=gen) < 0.4, -1.0, 1.0).cuda()
+    out, ht = gdr_ssm_forward(**d, softplus=False, cu_seqlens=[0, T], flags=flags)
+    gdr_device_check()
+    check(d, [T], out, ht, "bf16", CHUNKS, softplus=False)
+    # decays and growths of some 1.5 nats, 0.3 a token on the whole: chunks near the reference's range
+    # and beyond.  (The tokens of DROPS decay: 90 nats of growth would be no float32 number.)
+    d["dt"] = torch.where(d["dt"].abs() < 1, 30 * d["dt"], d["dt"].abs())
+    out, ht = gdr_ssm_forward(**d, softplus=False, cu_seqlens=[0, T], flags=flags)
+    gdr_device_check()
+    check(d, [T], out, ht, "bf16", CHUNKS, softplus=False)
