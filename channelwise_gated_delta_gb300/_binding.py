@@ -840,8 +840,8 @@ def gdr_ssm_forward(x, b, c, dt, a, d=None, z=None, dt_bias=None, cu_seqlens=Non
             if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
                 workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     if need:
-        if workspace.get_device() != index:
-            raise ValueError("workspace must be a CUDA tensor on cuda:%d" % index)
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on cuda:%d" % index)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = _on(index, lib.gdr_ssm_forward)(
         x.data_ptr(), b.data_ptr(), c.data_ptr(), dt_ptr, a_ptr, d_ptr, z_ptr, bias_ptr, h0_ptr,

@@ -46,3 +46,15 @@ def test_the_largest_ints_pass(monkeypatch):
     host = Host(monkeypatch)
     conv(*MOST[:2], out=MOST[2], store_st=False)
     assert host.calls[-1][0] == "gdr_short_conv"
+
+
+def test_a_workspace_that_is_less_than_it_counts(monkeypatch):
+    """One element expanded counts as many, and is no memory to write to."""
+    z = lambda *s, dt=bf16: OnGpu(torch.zeros(*s, dtype=dt))
+    args = [z(1, 3, 1, 32), z(1, 3, 1, 32), z(1, 3, 1, 32), z(1, 3, 1, dt=f32), z(1, dt=f32)]
+    host = Host(monkeypatch)
+    with pytest.raises(ValueError, match="contiguous"):
+        ssm(*args, workspace=OnGpu(torch.zeros(1, dtype=torch.uint8).expand(256)))
+    assert "gdr_ssm_forward" not in [c[0] for c in host.calls]
+    ssm(*args, workspace=OnGpu(torch.zeros(256, dtype=torch.uint8)))
+    assert host.calls[-1][0] == "gdr_ssm_forward"
