@@ -14,7 +14,7 @@ allocates are memory of that stream.
 """
 import contextlib
 import ctypes
-import math
+import decimal
 import os
 
 import torch
@@ -695,15 +695,26 @@ def gdr_short_conv(x, weight, bias=None, cu_seqlens=None, s0=None, out=None, st=
     return out, st
 
 
+_A_TURN = decimal.Decimal("0.159154943091895335768883763372514362034459645740456")  # of a radian
+
+
 def gdr_rope_freqs(d_rot, base=10000.0, inv_freq=None, device="cuda"):
     """The frequencies of gdr_qk_norm for ``d_rot`` rotated channels, int64 [d_rot / 2] in 2^-64
     turns a position: base^(-2 i / d_rot) radians for pair i, or ``inv_freq`` (radians a
-    position, one per pair)."""
-    if inv_freq is None:
-        inv_freq = [base ** (-2.0 * i / d_rot) for i in range(d_rot // 2)]
-    elif len(inv_freq) != d_rot // 2:
+    position, one per pair).  Rounded once: a float64 frequency would be off by 2^-53 of itself, and
+    the angle at position 2^31 by 2^-22 radians."""
+    if inv_freq is not None and len(inv_freq) != d_rot // 2:
         raise ValueError("inv_freq must have d_rot / 2 entries")
-    turns = [int(float(f) / (2.0 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for f in inv_freq]
+    with decimal.localcontext(decimal.Context(prec=50)):
+        unit = _A_TURN * 2 ** 64
+        if inv_freq is None:
+            turns, ratio = [unit], decimal.Decimal(base) ** (decimal.Decimal(-2) / max(d_rot, 1))
+            while len(turns) < d_rot // 2:
+                turns.append(turns[-1] * ratio)
+            turns = turns[:d_rot // 2]
+        else:
+            turns = [decimal.Decimal(float(f)) * unit for f in inv_freq]
+        turns = [int(t.to_integral_value()) & (2 ** 64 - 1) for t in turns]
     return torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64,
                         device=device)
 
