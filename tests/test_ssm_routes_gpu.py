@@ -63,3 +63,18 @@ def test_a_z_that_tma_cannot_read(dv, flags, first, apart):
     if not generic:   # the same bits as with a z that it can read
         same, end = gdr_ssm_forward(**d, cu_seqlens=spread(lens), flags=flags)
         assert torch.equal(out, same) and torch.equal(ht, end)
+
+
+def test_long_runs_are_alike():
+    """Many CTAs over many chunks, other work between: the same bits each time."""
+    N, T, HK, HV, D = 4, 4096, 16, 32, 128
+    sets = []
+    for seed in range(2):
+        d = draw([T] * N, HK, HV, D, D, "bf16", seed=seed, z=seed == 1)
+        sets.append({k: v.unflatten(0, (N, T)) if k in ("x", "b", "c", "dt", "z") and v is not None else v
+                     for k, v in d.items()})
+    want = [[t.clone() for t in gdr_ssm_forward(**d)] for d in sets]
+    for _ in range(5):
+        for d, w in zip(sets, want):
+            assert all(torch.equal(p, q) for p, q in zip(gdr_ssm_forward(**d), w))
+    gdr_device_check()
