@@ -7,8 +7,8 @@
 // registers), their taps and the last W - 1 rows in registers and walks `rows`
 // rows of a sequence; kStep rows are in flight at a time.  The rows before its
 // first are read again (W - 1 of `rows`).  65536 rows of 8192 channels in bf16
-// take 331 us, 6.5 TB/s (468 us without the rows ahead; a copy runs at 6.8), where
-// the issue slots are 64 % busy.  Channels in odd numbers or rows at odd distances
+// take 328 us, 6.5 TB/s (468 us without the rows ahead; a copy runs at 6.8), where
+// the issue slots are 62 % busy.  Channels in odd numbers or rows at odd distances
 // are taken one a thread: 8192 rows of 8192 take 92 us so, 51 us by four.
 #include <stdint.h>
 

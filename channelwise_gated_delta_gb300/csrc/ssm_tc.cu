@@ -50,8 +50,8 @@
 //            ahead), and a thread that waits for one product's inputs feeds no other
 // The chain's registers (112 a thread) come from the others (56).
 //
-// What bounds it: 4 x 16384 tokens of 32 heads of 128 take 400 us, 3000 cycles a
-// chunk.  Its products take 1790 of them, its bytes 1820 (at 6.8 TB/s).
+// What bounds it: 4 x 16384 tokens of 32 heads of 128 take 395 us, 3000 cycles a
+// chunk (629 where every chunk of a head is beyond r's range).  Its products take 1790 of them, its bytes 1820 (at 6.8 TB/s).
 // The rest is one chunk's way around: products of dS 770, its read 200, S 600 to
 // 900, the next products' start 200, with the other products in between.  With
 // all arithmetic of the warps taken out it takes 380.

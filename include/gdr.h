@@ -531,7 +531,8 @@ GDR_API gdr_status gdr_state_load(const signed char *cache, const float *scale, 
  *
  * gdr_short_conv: a causal convolution of each channel with W taps,
  *     out[t][c] = act(bias[c] + sum_j w[c][j] x[t - W + 1 + j][c]),
- * act = silu(y) = y / (1 + exp(-y)) with GDR_FLAG_SILU, else nothing.
+ * act = silu(y) = y / (1 + exp(-y)) with GDR_FLAG_SILU, else nothing.  (It is 0
+ * below y = -87.3, where silu is nearer to 0 than 2^-119.)
  *
  *   x, out      [rows][D], rows ldx and ldo elements apart, dtype
  *   w, bias     float32 [D][W] and [D]; bias may be NULL
@@ -570,7 +571,8 @@ GDR_API gdr_status gdr_short_conv(const void *x, const float *w, const float *bi
  *               a far position is as exact as that of a near one
  *
  * Computed in float32 and rounded once.  The sum of squares of a head has to
- * fit float32 (a head beyond that comes out as zeros).  Supported: rows >= 0,
+ * fit float32 (a head beyond that comes out as zeros), and where eps is not
+ * larger, to be a normal number (values below 2^-60 lose digits).  Supported: rows >= 0,
  * HQ, HK >= 1, d in {32, 64, 128, 256}, d_rot <= d a multiple of 16, eps >= 0.
  * Tensors 16-byte aligned and ld* multiples of 16 bytes, weights and positions
  * 4-byte, freqs 8-byte aligned.  flags: the two above or 0.
@@ -608,7 +610,8 @@ GDR_API gdr_status gdr_qk_norm(const void *q, const void *k, const float *weight
  * rounded; bf16 sequences run by chunks of 64 tokens on the tensor cores (x, b
  * and c 16-byte aligned, their distances multiples of 16 bytes; otherwise token by
  * token, as f32 and short ones), where the outputs read a copy of the state
- * rounded to bf16 and what a token adds to the state is off by 8e-7 of it (rms).  A value that is not finite reaches no output of an earlier
+ * rounded to bf16 (off by up to 2^-8 of the sum of the sizes of its products with c) and what a token
+ * adds to the state is off by 8e-7 of it (rms).  silu as in gdr_short_conv.  A value that is not finite reaches no output of an earlier
  * token; from there on its column (x, z) or head comes out as NaN or infinite.
  * A chunk's outputs are formed about the middle of its decay: where a head decays to 2^-n over a
  * chunk, n <= 160, the sum over its tokens of |x| (|c . b| step + |D|) has to stay below 2^(127 - n/2)
